@@ -26,7 +26,9 @@ EXPORTS = ["hyena_version", "hyena_status_string", "hyena_last_error_detail", "h
            "hyena_gated_fftconv_workspace_min_bytes", "hyena_gated_fftconv", "hyena_gated_fftconv_noalloc",
            "hyena_gated_fftconv_per_sample", "hyena_gated_fftconv_host", "hyena_spectrum_check",
            "hyena_debug_conv_tc", "hyena_debug_conv_cluster", "hyena_debug_conv_2d_tc", "hyena_debug_conv_2dc_tc", "hyena_gated_fftconv_ex", "hyena_kernel_status", "hyena_in_proj",
-           "hyena_out_proj", "hyena_implicit_filter_workspace_bytes", "hyena_filter_spectrum_implicit"]
+           "hyena_out_proj", "hyena_implicit_filter_workspace_bytes", "hyena_filter_spectrum_implicit",
+           "hyena_delta_rule_workspace_bytes", "hyena_delta_rule", "hyena_delta_rule_step", "hyena_quantize_fp8",
+           "hyena_quantize_fp8_weight", "hyena_proj_fp8"]
 
 _lock = threading.Lock()
 _lib = None
@@ -106,6 +108,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.hyena_debug_conv_2dc_tc.restype = ctypes.c_int
         lib.hyena_debug_conv_2dc_tc.argtypes = [vp, vp, vp, sz, i64, i64, ctypes.c_int, vp, sz,
                                                 ctypes.c_uint64, ctypes.c_int, vp]
+        lib.hyena_delta_rule_workspace_bytes.restype = sz
+        lib.hyena_delta_rule_workspace_bytes.argtypes = [i64, i64] + [ctypes.c_int] * 5
+        lib.hyena_delta_rule.restype = ctypes.c_int
+        lib.hyena_delta_rule.argtypes = [ctypes.POINTER(DeltaRule), vp, sz, vp]
+        lib.hyena_delta_rule_step.restype = ctypes.c_int
+        lib.hyena_delta_rule_step.argtypes = [ctypes.POINTER(DeltaRule), vp, i64, vp, vp]
+        lib.hyena_quantize_fp8.restype = ctypes.c_int
+        lib.hyena_quantize_fp8.argtypes = [vp, vp, fp, i64, i64, i64, ctypes.c_int, ctypes.c_int, vp]
+        lib.hyena_quantize_fp8_weight.restype = ctypes.c_int
+        lib.hyena_quantize_fp8_weight.argtypes = [vp, vp, fp, i64, i64, ctypes.c_int, vp]
+        lib.hyena_proj_fp8.restype = ctypes.c_int
+        lib.hyena_proj_fp8.argtypes = [vp, fp, vp, fp, fp, vp, i64, i64, i64, i64, ctypes.c_int, vp]
         _lib = lib
     return _lib
 
@@ -259,9 +273,146 @@ def hyena_filter_spectrum_implicit(params: dict, D, C: int, L: int, order: int, 
                                                  ws_bytes, _ptr(k_out), _stream(stream)))
 
 
+HYENA_DELTA_L2NORM = 0x1
+
+
+class DeltaRule(ctypes.Structure):
+    """hyena_delta_rule_t (device pointers, element strides)."""
+    _fields_ = ([("B", ctypes.c_int64), ("L", ctypes.c_int64)]
+                + [(n, ctypes.c_int) for n in ("Hk", "Hv", "dk", "dv", "dtype")]
+                + [("flags", ctypes.c_uint), ("scale", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "g", "beta")]
+                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride", "g_stride",
+                                                     "beta_stride")]
+                + [(n, ctypes.c_void_p) for n in ("state_in", "state_out", "lengths")])
+
+
+def _on_device(*tensors) -> None:
+    """The kernels run on the current device: its own tensors only."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _plain(name, t, shape, dtype) -> None:
+    """A contiguous tensor of this shape and dtype (None passes)."""
+    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, three) -> DeltaRule:
+    """Shapes checked, tensors and strides into the struct.  three: [B, C, L]
+    and [B, Hv, L]; otherwise [B, C] and [B, Hv]."""
+    import torch
+    if Hk < 1 or Hv < 1 or q.shape[1] % Hk or v.shape[1] % Hv:
+        raise ValueError("the channels of q and k must divide into Hk heads, those of v into Hv")
+    dk, dv = q.shape[1] // Hk, v.shape[1] // Hv
+    tail = (L,) if three else ()
+    for name, t, c in (("q", q, Hk * dk), ("k", k, Hk * dk), ("v", v, Hv * dv), ("o", o, Hv * dv)):
+        if tuple(t.shape) != (B, c) + tail or t.dtype != q.dtype:
+            raise ValueError(f"{name} must be {q.dtype} {(B, c) + tail}, got {t.dtype} {tuple(t.shape)}")
+    for name, t in (("g", g), ("beta", beta)):
+        if t is not None and (tuple(t.shape) != (B, Hv) + tail or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be float32 {(B, Hv) + tail}, got {t.dtype} {tuple(t.shape)}")
+    i3 = ctypes.c_int64 * 3
+
+    def stride(t):                                   # two strides: the third, of the one token, stays 0
+        return i3(*t.stride()) if t is not None else i3()
+
+    return DeltaRule(B, L, Hk, Hv, dk, dv, _dtype_code(q), HYENA_DELTA_L2NORM if l2norm else 0,
+                     0.0 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(g),
+                     _ptr(beta), stride(q), stride(k), stride(v), stride(o), stride(g), stride(beta))
+
+
+def hyena_delta_rule_workspace_bytes(B: int, L: int, Hk: int, Hv: int, dk: int, dv: int, dtype) -> int:
+    """dtype: torch.float32 or torch.bfloat16, the storage of q, k, v, o."""
+    import torch
+    code = {torch.float32: HYENA_F32, torch.bfloat16: HYENA_BF16}[dtype]
+    return int(load().hyena_delta_rule_workspace_bytes(B, L, Hk, Hv, dk, dv, code))
+
+
+def hyena_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in=None, state_out=None, lengths=None, scale=None,
+                     l2norm: bool = False, workspace=None, stream=None) -> None:
+    """q, k: [B, Hk*dk, L], v, o: [B, Hv*dv, L] (f32 or bf16, any strides: views
+    of a projected stream; token-major tensors as x.transpose(1, 2)), g, beta:
+    [B, Hv, L] f32 or None, state_in/state_out: [B, Hv, dk, dv] f32 or None,
+    lengths: [B] int32 or None, workspace: uint8 of
+    hyena_delta_rule_workspace_bytes(...) or None when that is 0."""
+    import torch
+    _on_device(q, k, v, g, beta, o, state_in, state_out, lengths, workspace)
+    B, _, L = q.shape
+    a = _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, True)
+    _plain("state_in", state_in, (B, Hv, a.dk, a.dv), torch.float32)
+    _plain("state_out", state_out, (B, Hv, a.dk, a.dv), torch.float32)
+    _plain("lengths", lengths, (B,), torch.int32)
+    a.state_in, a.state_out, a.lengths = _ptr(state_in), _ptr(state_out), _ptr(lengths)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().hyena_delta_rule(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def hyena_delta_rule_step(q, k, v, g, beta, o, states, Hk: int, Hv: int, slots=None, scale=None, l2norm: bool = False,
+                          stream=None) -> None:
+    """One token a row: q, k: [B, Hk*dk], v, o: [B, Hv*dv], g, beta: [B, Hv] or
+    None, states: [n, Hv, dk, dv] f32 updated in place, slots: [B] int32 (row b
+    uses state slots[b], negative: padding) or None (row b uses state b)."""
+    import torch
+    _on_device(q, k, v, g, beta, o, states, slots)
+    B = q.shape[0]
+    a = _delta_args(q, k, v, g, beta, o, B, 1, Hk, Hv, scale, l2norm, False)
+    _plain("states", states, (states.shape[0], Hv, a.dk, a.dv), torch.float32)
+    _plain("slots", slots, (B,), torch.int32)
+    _check(load().hyena_delta_rule_step(ctypes.byref(a), states.data_ptr(), states.shape[0], _ptr(slots),
+                                        _stream(stream)))
+
+
+def hyena_quantize_fp8(x, xq, xs, channels_first: bool = False, stream=None) -> None:
+    """x [B, L, K] (or [B, K, L] with channels_first) f32 or bf16 -> xq [B, L, K]
+    float8_e4m3fn, xs [B, ceil(K/128), L] f32."""
+    import torch
+    _on_device(x, xq, xs)
+    B, L, K = (x.shape[0], x.shape[2], x.shape[1]) if channels_first else x.shape
+    _plain("x", x, tuple(x.shape), x.dtype)
+    _plain("xq", xq, (B, L, K), torch.float8_e4m3fn)
+    _plain("xs", xs, (B, -(-K // 128), L), torch.float32)
+    _check(load().hyena_quantize_fp8(x.data_ptr(), xq.data_ptr(), xs.data_ptr(), B, L, K, _dtype_code(x),
+                                     1 if channels_first else 0, _stream(stream)))
+
+
+def hyena_quantize_fp8_weight(W, Wq, Ws, stream=None) -> None:
+    """W [N, K] f32 or bf16 -> Wq [N, K] float8_e4m3fn, Ws [ceil(N/128), ceil(K/128)] f32."""
+    import torch
+    _on_device(W, Wq, Ws)
+    N, K = W.shape
+    _plain("W", W, (N, K), W.dtype)
+    _plain("Wq", Wq, (N, K), torch.float8_e4m3fn)
+    _plain("Ws", Ws, (-(-N // 128), -(-K // 128)), torch.float32)
+    _check(load().hyena_quantize_fp8_weight(W.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), N, K, _dtype_code(W),
+                                            _stream(stream)))
+
+
+def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stream=None) -> None:
+    """xq [B, L, K], Wq [N, K] float8_e4m3fn with their scales, bias [N] f32 or
+    None -> out bf16 [B, L, N], or [B, N, L] with channels_first."""
+    import torch
+    _on_device(xq, xs, Wq, Ws, bias, out)
+    B, L, K = xq.shape
+    N = Wq.shape[0]
+    _plain("xq", xq, (B, L, K), torch.float8_e4m3fn)
+    _plain("xs", xs, (B, -(-K // 128), L), torch.float32)
+    _plain("Wq", Wq, (N, K), torch.float8_e4m3fn)
+    _plain("Ws", Ws, (-(-N // 128), -(-K // 128)), torch.float32)
+    _plain("bias", bias, (N,), torch.float32)
+    _plain("out", out, (B, N, L) if channels_first else (B, L, N), torch.bfloat16)
+    _check(load().hyena_proj_fp8(xq.data_ptr(), xs.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), _ptr(bias),
+                                 out.data_ptr(), B, L, K, N, 1 if channels_first else 0, _stream(stream)))
+
+
 def hyena_kernel_status(stream=None) -> None:
-    """Raises HyenaError (HYENA_ERR_TIMEOUT or HYENA_ERR_SPECTRUM_MISMATCH)
-    when a convolution kernel on the current device recorded one since the
+    """Raises HyenaError (HYENA_ERR_TIMEOUT, HYENA_ERR_SPECTRUM_MISMATCH, or
+    HYENA_ERR_INVALID_ARG for a bad slot of hyena_delta_rule_step)
+    when a kernel on the current device recorded one since the
     last call; synchronises the stream and clears the record."""
     _check(load().hyena_kernel_status(_stream(stream)))
 

@@ -18,6 +18,8 @@ constexpr uint64_t kDefaultWaitBudgetNs = 2000000000ull;
 constexpr uint32_t kStatusTimeout = 1u;            // a bounded tensor-core wait ran out
 constexpr uint32_t kStatusSpectrumMismatch = 2u;   // spectrum header does not match the launch
 
+constexpr uint32_t kStatusBadSlot = 4u;            // a state slot out of range, or named twice
+
 // Device address of this device's kernel status word (looked up once per device).
 cudaError_t kernel_status_word(uint32_t** out);
 

@@ -39,10 +39,27 @@
 #include "hyena.h"
 #include "kernels.h"
 #include "tc_util.cuh"
+#include "tma_util.cuh"
 
 namespace hyena {
 
 hyena_status_t set_last_error_detail(hyena_status_t st, const std::string& detail);  // api.cu
+
+cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+    static std::mutex mutex;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorSymbolNotFound;
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    *out = encode;
+    return cudaSuccess;
+}
 
 namespace {
 
@@ -85,37 +102,6 @@ struct GemmParams {
     uint64_t budget_ns;
     uint32_t* status;
 };
-
-// UMMA shared-memory descriptor, 128-byte swizzle (layout type 2), sm_100 version.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= uint64_t((saddr >> 4) & 0x3FFFu);
-    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
-    d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
-    d |= uint64_t(1) << 46;
-    d |= uint64_t(2) << 61;
-    return d;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                            uint64_t* mbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
-            "r"(tc::smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(mbar))
-        : "memory");
-}
-
-__device__ __forceinline__ void commit_to(uint64_t* mbar) { tc::commit(mbar); }
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* mbar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(mbar)) : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&h);
-}
 
 template <int BN>
 __global__ void __launch_bounds__(kThreadsG, 1)
@@ -179,12 +165,12 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     const int k0 = kb * BK;
                     if (p.a_mn_major) {
                         // two 64-row (m) halves of the 128-row tile, each [64 k][64 m]
-                        tma_load_3d(sa, &map_a, m0, k0, p.a_batched ? int(b) : 0, &full[s]);
-                        tma_load_3d(sa + kATile / 2, &map_a, m0 + 64, k0, p.a_batched ? int(b) : 0, &full[s]);
+                        tc::tma_load_3d(sa, &map_a, m0, k0, p.a_batched ? int(b) : 0, &full[s]);
+                        tc::tma_load_3d(sa + kATile / 2, &map_a, m0 + 64, k0, p.a_batched ? int(b) : 0, &full[s]);
                     } else {
-                        tma_load_3d(sa, &map_a, k0, m0, p.a_batched ? int(b) : 0, &full[s]);
+                        tc::tma_load_3d(sa, &map_a, k0, m0, p.a_batched ? int(b) : 0, &full[s]);
                     }
-                    tma_load_3d(sb, &map_b, k0, n0, p.b_batched ? int(b) : 0, &full[s]);
+                    tc::tma_load_3d(sb, &map_b, k0, n0, p.b_batched ? int(b) : 0, &full[s]);
                 }
             }
             if (!ok) report_status(p.status, kStatusTimeout);
@@ -221,19 +207,19 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     for (int ks = 0; ks < BK / 16; ++ks) {
                         // K-major: +32 bytes per 16 elements inside the 128-byte row;
                         // MN-major A: +2 groups of 8 k-rows (1024 bytes each)
-                        const uint64_t da = p.a_mn_major ? desc_sw128(sa + uint32_t(ks) * 2048u, kATile / 2, 1024)
-                                                         : desc_sw128(sa + uint32_t(ks) * 32u, 16, 1024);
-                        const uint64_t db = desc_sw128(sb + uint32_t(ks) * 32u, 16, 1024);
+                        const uint64_t da = p.a_mn_major ? tc::desc_sw128(sa + uint32_t(ks) * 2048u, kATile / 2, 1024)
+                                                         : tc::desc_sw128(sa + uint32_t(ks) * 32u, 16, 1024);
+                        const uint64_t db = tc::desc_sw128(sb + uint32_t(ks) * 32u, 16, 1024);
                         tc::mma_bf16(d_tmem, da, db, idesc, (kb > 0 || ks > 0) ? 1u : 0u);
                     }
-                    commit_to(&empty[s]);             // the stage is free once these MMAs have read it
+                    tc::commit(&empty[s]);             // the stage is free once these MMAs have read it
                 }
                 if (!ok) break;
-                commit_to(&acc_full[acc]);            // the tile's accumulator is complete
+                tc::commit(&acc_full[acc]);            // the tile's accumulator is complete
             }
             if (!ok) report_status(p.status, kStatusTimeout);
             // nothing left in flight before tensor memory is released
-            commit_to(mma_done);
+            tc::commit(mma_done);
             if (!tc::mbar_wait(mma_done, 0, p.budget_ns)) report_status(p.status, kStatusTimeout);
         }
     } else {
@@ -280,8 +266,8 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         *reinterpret_cast<uint4*>(sw + lane * kEpiRow + 16 * c) =
-                            make_uint4(pack2(v[8 * c], v[8 * c + 1]), pack2(v[8 * c + 2], v[8 * c + 3]),
-                                       pack2(v[8 * c + 4], v[8 * c + 5]), pack2(v[8 * c + 6], v[8 * c + 7]));
+                            make_uint4(tc::pack2(v[8 * c], v[8 * c + 1]), tc::pack2(v[8 * c + 2], v[8 * c + 3]),
+                                       tc::pack2(v[8 * c + 4], v[8 * c + 5]), tc::pack2(v[8 * c + 6], v[8 * c + 7]));
                     __syncwarp();
                     // round k: rows 4 k + lane / 8, 16-byte chunk lane % 8 of the 64 columns
 #pragma unroll
@@ -311,8 +297,8 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         if (n + 8 * g + 8 <= p.N) {
-                            const uint4 w = make_uint4(pack2(v[8 * g], v[8 * g + 1]), pack2(v[8 * g + 2], v[8 * g + 3]),
-                                                       pack2(v[8 * g + 4], v[8 * g + 5]), pack2(v[8 * g + 6], v[8 * g + 7]));
+                            const uint4 w = make_uint4(tc::pack2(v[8 * g], v[8 * g + 1]), tc::pack2(v[8 * g + 2], v[8 * g + 3]),
+                                                       tc::pack2(v[8 * g + 4], v[8 * g + 5]), tc::pack2(v[8 * g + 6], v[8 * g + 7]));
                             *reinterpret_cast<uint4*>(cb + m * p.ldc + n + 8 * g) = w;
                         }
                     }
@@ -320,7 +306,7 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
+            if (lane == 0) tc::mbar_arrive(&acc_empty[acc]);
         }
         if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
     }
@@ -330,29 +316,12 @@ k_gemm_bf16(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------ host
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::mutex g_encode_mutex;
-
-cudaError_t encode_fn(PFN_cuTensorMapEncodeTiled_v12000* out) {
-    std::lock_guard<std::mutex> lock(g_encode_mutex);
-    if (!g_encode) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorSymbolNotFound;
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
-    *out = g_encode;
-    return cudaSuccess;
-}
-
 // 3-D bf16 tensor map, dims (d0 innermost, d1, d2), byte strides of d1 and d2,
 // box (b0, b1, 1), 128-byte swizzle; out-of-range elements read as zero.
 bool make_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
               uint32_t b0, uint32_t b1, std::string* why) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-    cudaError_t e = encode_fn(&enc);
+    cudaError_t e = tensor_map_encoder(&enc);
     if (e != cudaSuccess) {
         *why = std::string("cuTensorMapEncodeTiled unavailable: ") + cudaGetErrorString(e);
         return false;

@@ -10,6 +10,8 @@
 //          row pair it was on are NaN; nothing was left in flight)
 //   bit 1  a convolution kernel found a spectrum whose header does not match
 //          the shape it was launched for (that kernel wrote no output)
+//   bit 2  the delta rule's step found a state slot that is out of range or
+//          named by two rows (NaN outputs for that row, no state written)
 // The bits are sticky until hyena_kernel_status clears them.  Kernels in the
 // other translation units get the word's device address as an argument; it
 // is looked up once per device (cudaGetSymbolAddress with that device
@@ -74,5 +76,9 @@ extern "C" hyena_status_t hyena_kernel_status(void* stream) {
                                             "a convolution kernel found a spectrum header that does not match its "
                                             "shape (never filled, or filled for another C, size or order); its "
                                             "output was not written");
+    if (bits & hyena::kStatusBadSlot)
+        return hyena::set_last_error_detail(HYENA_ERR_INVALID_ARG,
+                                            "hyena_delta_rule_step found a slot that names no state, or a state named "
+                                            "by two rows; the outputs of that row were written as NaN");
     return hyena::set_last_error_detail(HYENA_OK, "");
 }

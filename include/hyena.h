@@ -281,7 +281,9 @@ hyena_status_t hyena_gated_fftconv_ex(const void* u, void* y, const void* spectr
  * nothing in flight) or HYENA_ERR_SPECTRUM_MISMATCH (a kernel found a
  * spectrum header that does not match the shape it was given -- never
  * filled, or filled for another C, size or order of the same byte size --
- * and wrote no output), or HYENA_ERR_CUDA.  The word is per device, not per
+ * and wrote no output), HYENA_ERR_INVALID_ARG (a slot of
+ * hyena_delta_rule_step that names no state, or one named twice), or
+ * HYENA_ERR_CUDA.  The word is per device, not per
  * stream or per call: kernels running on other streams meanwhile may set
  * bits between the read and the clear, and those bits are lost.  Its address
  * is looked up once per device (calls after a device reset are not
@@ -381,6 +383,136 @@ hyena_status_t hyena_in_proj(const void* x, const void* W, const float* bias, vo
  */
 hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, void* out, int64_t B, int64_t L,
                               int64_t D, void* stream);
+
+/*
+ * hyena_delta_rule -- the gated delta rule over whole sequences: a token mixer
+ * that stands where the gated long convolution does, between the projections.
+ * The pages have no counterpart.
+ *
+ * Per batch row b and value head h (key head h / (Hv / Hk)), a state S [dk, dv]:
+ *   S   <- exp(g_t) S
+ *   u_t  = beta_t (v_t - S^T k_t)
+ *   S   <- S + k_t u_t^T
+ *   o_t  = scale S^T q_t
+ * With HYENA_DELTA_L2NORM, q_t and k_t are first divided by
+ * sqrt(sum_i x_i^2 + 1e-6), head by head.
+ *
+ * q, k, v and o are [B, H d, L] tensors given by a pointer and three element
+ * strides (batch, channel, time), so the channel blocks of a projected stream
+ * ([B, Ctot, L], or token by token [B, L, Ctot]) serve in place; channel
+ * h * d + i is component i of head h.  g and beta are fp32 [B, Hv, L] with
+ * strides (batch, head, time).
+ *
+ *   g         log decay, <= 0 for a decaying state (-inf empties it); NULL = 0
+ *   beta      write strength; NULL = 1
+ *   state_in  [B, Hv, dk, dv] fp32, contiguous, the state before the first
+ *             token, or NULL (= 0)
+ *   state_out [B, Hv, dk, dv] fp32, receives the state after the last token,
+ *             or NULL; may be state_in itself
+ *   lengths   [B] int32 on the device, or NULL: row b has only its first
+ *             lengths[b] tokens (clamped to [0, L]).  What lies behind them is
+ *             not read into any result, whatever it holds, and o is left as it
+ *             was there; the state is that after the last token (length 0: the
+ *             state before the first).
+ *   scale     0 selects dk^-0.5
+ *   dtype     storage of q, k, v, o.  The state, g, beta and every sum are fp32.
+ *             HYENA_F32 runs token by token in fp32 on the CUDA cores.
+ *
+ * 1 <= dk <= 128, 1 <= dv <= 256, Hv a multiple of Hk, B <= 65535, L <= 2^30,
+ * Hv <= 4096.  q, k, v and o may start at any element (alignment of the
+ * dtype); states are 16-byte aligned, g, beta and lengths 4-byte.  Input
+ * strides are >= 0, those of o must give every element a place of its own, and
+ * the memory range of o (and of state_out) may not overlap that of another
+ * operand.
+ * workspace: hyena_delta_rule_workspace_bytes() bytes, 16-byte aligned (NULL
+ * when that is 0); its contents are undefined after the call, and two calls
+ * that may run at the same time need one each.  Asynchronous on `stream`,
+ * may be captured into a graph.
+ */
+#define HYENA_DELTA_L2NORM 0x1u
+
+typedef struct {
+    int64_t B, L;
+    int Hk, Hv, dk, dv;
+    int dtype;                 /* hyena_dtype_t */
+    unsigned flags;            /* HYENA_DELTA_L2NORM */
+    float scale;
+    const void *q, *k, *v;
+    void* o;
+    const float *g, *beta;
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    int64_t g_stride[3], beta_stride[3];
+    const float* state_in;
+    float* state_out;
+    const int32_t* lengths;
+} hyena_delta_rule_t;
+
+/* Workspace bytes of hyena_delta_rule (0 where none is needed, and for unsupported arguments). */
+size_t hyena_delta_rule_workspace_bytes(int64_t B, int64_t L, int Hk, int Hv, int dk, int dv, hyena_dtype_t dtype);
+
+hyena_status_t hyena_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * hyena_delta_rule_step -- one token of every sequence, the states updated in
+ * place (generation).
+ *
+ * p as in hyena_delta_rule with L = 1 and state_in, state_out and lengths NULL.
+ *   states   [n_states, Hv, dk, dv] fp32, contiguous, read and written
+ *   slots    [B] int32 on the device, or NULL (row b uses state b).  Row b uses
+ *            state slots[b]; a negative slot marks a row of padding: its o is
+ *            left as it was.  States that no row names are left as they were.
+ * A slot >= n_states, or one that an earlier row named already, cannot be
+ * refused before the launch: the kernel writes NaN to that row's o, touches no
+ * state for it, and hyena_kernel_status returns HYENA_ERR_INVALID_ARG.
+ */
+hyena_status_t hyena_delta_rule_step(const hyena_delta_rule_t* p, float* states, int64_t n_states,
+                                     const int32_t* slots, void* stream);
+
+/*
+ * hyena_quantize_fp8 -- activations to e4m3 with one fp32 scale for each row
+ * and block of 128 channels (the x operand of hyena_proj_fp8).  The pages have
+ * no counterpart.
+ *
+ *   x   [B, L, K] (channels_first = 0) or [B, K, L] (channels_first = 1: the
+ *       mixers' output, read in place), contiguous, dtype
+ *   xq  [B, L, K] e4m3 out
+ *   xs  [B, ceil(K/128), L] fp32 out
+ *   xs = max(amax / 448, 2^-126) over the block's |x|, xq = x / xs rounded to
+ *   nearest even; amax / 448 and x / xs are fp32 numbers (round to nearest).
+ * A block that holds an infinity or a NaN gets scale infinity or NaN, so every
+ * value it stands for is NaN.  K a multiple of 16, B <= 65535; x, xq
+ * 16-byte aligned, xs 4-byte; outputs may not overlap x.
+ */
+hyena_status_t hyena_quantize_fp8(const void* x, void* xq, float* xs, int64_t B, int64_t L, int64_t K,
+                                  hyena_dtype_t dtype, int channels_first, void* stream);
+
+/*
+ * hyena_quantize_fp8_weight -- the same for a weight W [N, K] (out x in), one
+ * scale for each block of 128 x 128: Wq [N, K] e4m3, Ws [ceil(N/128),
+ * ceil(K/128)] fp32.  Once a weight.
+ */
+hyena_status_t hyena_quantize_fp8_weight(const void* W, void* Wq, float* Ws, int64_t N, int64_t K,
+                                         hyena_dtype_t dtype, void* stream);
+
+/*
+ * hyena_proj_fp8 -- a projection (hyena_in_proj, hyena_out_proj) on 8-bit
+ * operands with a scale for each block of 128:
+ *   out[b][l][n] = sum_kb xs[b][kb][l] Ws[n/128][kb]
+ *                  sum_{k in block kb} xq[b][l][k] Wq[n][k]  + bias[n]
+ *
+ *   xq, xs  from hyena_quantize_fp8: [B, L, K] e4m3, [B, ceil(K/128), L] fp32
+ *   Wq, Ws  from hyena_quantize_fp8_weight: [N, K] e4m3, [ceil(N/128), ceil(K/128)]
+ *   bias    [N] fp32, or NULL (= 0)
+ *   out     bf16, [B, N, L] (channels_first = 1: what hyena_shortconv and the
+ *           mixers read) or [B, L, N] (channels_first = 0)
+ * Products and sums are fp32, the result is rounded once (to nearest even).
+ * K a multiple of 16, L and N any, B <= 65535, B * L <= 2^31 - 1, N and K <= 2^20; xq, Wq, out
+ * 16-byte aligned, xs, Ws, bias 4-byte; out may not overlap an input.  A
+ * bounded device wait that runs out is reported by hyena_kernel_status.
+ */
+hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws, const float* bias,
+                              void* out, int64_t B, int64_t L, int64_t K, int64_t N, int channels_first,
+                              void* stream);
 
 /*
  * Size of the fixed scratch array used by hyena_gated_fftconv_noalloc (32 MiB).
