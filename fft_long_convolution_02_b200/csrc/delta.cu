@@ -346,6 +346,23 @@ bool shapes_ok(int64_t B, int64_t L, int Hk, int Hv, int dk, int dv) {
            Hv % Hk == 0 && dk >= 1 && dk <= kDeltaMaxDk && dv >= 1 && dv <= kDeltaMaxDv;
 }
 
+// Whether a range meets any operand of *p (its strides and sizes checked).
+bool meets_operand(const Range& r, const hyena_delta_rule_t* p) {
+    const int64_t es = p->dtype == HYENA_BF16 ? 2 : 4;
+    const int64_t Ck = int64_t(p->Hk) * p->dk, Cv = int64_t(p->Hv) * p->dv, n = p->B * p->Hv * p->dk * int64_t(p->dv) * 4;
+    auto flat = [](const void* q, int64_t bytes) { return Range{static_cast<const char*>(q), static_cast<const char*>(q) + bytes}; };
+    return r.meets(range_of(p->q, p->B, Ck, p->L, p->q_stride, es)) || r.meets(range_of(p->k, p->B, Ck, p->L, p->k_stride, es)) ||
+           r.meets(range_of(p->v, p->B, Cv, p->L, p->v_stride, es)) || r.meets(range_of(p->o, p->B, Cv, p->L, p->o_stride, es)) ||
+           (p->g && r.meets(range_of(p->g, p->B, p->Hv, p->L, p->g_stride, 4))) ||
+           (p->beta && r.meets(range_of(p->beta, p->B, p->Hv, p->L, p->beta_stride, 4))) ||
+           (p->state_in && r.meets(flat(p->state_in, n))) || (p->state_out && r.meets(flat(p->state_out, n))) ||
+           (p->lengths && r.meets(flat(p->lengths, 4 * p->B)));
+}
+
+// bf16 storage runs in chunks from a few tokens on; below, one launch of the token-by-token kernel is sooner done.
+constexpr int64_t kSeqMost = 16;
+bool chunked(int64_t L, int dtype) { return dtype == HYENA_BF16 && L > kSeqMost; }
+
 // Checks shared by both entry points; fills the launch arguments.
 hyena_status_t prepare_delta(const hyena_delta_rule_t* p, DeltaArgs* a) {
     if (!p) return fail(HYENA_ERR_INVALID_ARG, "the argument struct is NULL");
@@ -434,17 +451,28 @@ using namespace hyena;
 
 extern "C" size_t hyena_delta_rule_workspace_bytes(int64_t B, int64_t L, int Hk, int Hv, int dk, int dv,
                                                    hyena_dtype_t dtype) {
-    (void)B, (void)L, (void)Hk, (void)Hv, (void)dk, (void)dv, (void)dtype;
-    return 0;
+    if (!shapes_ok(B, L, Hk, Hv, dk, dv) || !chunked(L, dtype)) return 0;
+    return delta_chunk_workspace(B, L, Hv);
 }
 
 extern "C" hyena_status_t hyena_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
                                            void* stream) {
-    (void)workspace, (void)workspace_bytes;
     DeltaArgs a;
     hyena_status_t st = prepare_delta(p, &a);
     if (st != HYENA_OK) return st;
-    return done(launch_delta_seq(a, p->dtype, static_cast<cudaStream_t>(stream)), "delta rule");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!chunked(p->L, p->dtype)) return done(launch_delta_seq(a, p->dtype, s), "delta rule");
+    const size_t need = delta_chunk_workspace(p->B, p->L, p->Hv);
+    if (!workspace || workspace_bytes < need)
+        return fail(HYENA_ERR_WORKSPACE_TOO_SMALL, "workspace must hold at least " + std::to_string(need) + " bytes");
+    if (!aligned(workspace, 16)) return fail(HYENA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    const char* w = static_cast<const char*>(workspace);
+    const Range wr{w, w + need};
+    if (meets_operand(wr, p)) return fail(HYENA_ERR_INVALID_ARG, "workspace overlaps an operand");
+    uint32_t* status = nullptr;
+    cudaError_t e = kernel_status_word(&status);
+    if (e != cudaSuccess) return done(e, "kernel status word");
+    return done(launch_delta_chunk(a, workspace, status, s), "delta rule");
 }
 
 extern "C" hyena_status_t hyena_delta_rule_step(const hyena_delta_rule_t* p, float* states, int64_t n_states,
@@ -460,17 +488,11 @@ extern "C" hyena_status_t hyena_delta_rule_step(const hyena_delta_rule_t* p, flo
         return fail(HYENA_ERR_MISALIGNED, "states must be 16-byte aligned, slots 4-byte");
     if (n_states < 1 || (!slots && n_states < p->B) || n_states > (int64_t(1) << 31))
         return fail(HYENA_ERR_INVALID_ARG, "n_states must be >= 1, and >= B without slots");
-    const int64_t es = p->dtype == HYENA_BF16 ? 2 : 4;
-    const int64_t Ck = int64_t(p->Hk) * p->dk, Cv = int64_t(p->Hv) * p->dv;
     const char* sp = reinterpret_cast<const char*>(states);
     const char* lp = reinterpret_cast<const char*>(slots);
     const Range sr{sp, sp + n_states * p->Hv * p->dk * int64_t(p->dv) * 4}, lr{lp, lp + 4 * p->B};
-    const Range o = range_of(p->o, p->B, Cv, 1, p->o_stride, es);
-    if (sr.meets(o) || sr.meets(range_of(p->q, p->B, Ck, 1, p->q_stride, es)) ||
-        sr.meets(range_of(p->k, p->B, Ck, 1, p->k_stride, es)) || sr.meets(range_of(p->v, p->B, Cv, 1, p->v_stride, es)) ||
-        (p->g && sr.meets(range_of(p->g, p->B, p->Hv, 1, p->g_stride, 4))) ||
-        (p->beta && sr.meets(range_of(p->beta, p->B, p->Hv, 1, p->beta_stride, 4))) ||
-        (slots && (sr.meets(lr) || o.meets(lr))))
+    const Range o = range_of(p->o, p->B, int64_t(p->Hv) * p->dv, 1, p->o_stride, p->dtype == HYENA_BF16 ? 2 : 4);
+    if (meets_operand(sr, p) || (slots && (sr.meets(lr) || o.meets(lr))))
         return fail(HYENA_ERR_INVALID_ARG, "states or o overlaps another operand");
     uint32_t* status = nullptr;
     cudaError_t e = kernel_status_word(&status);

@@ -31,6 +31,9 @@ struct DeltaArgs {
 
 // Token by token (delta.cu): any strides, either storage type.
 cudaError_t launch_delta_seq(const DeltaArgs& a, int dtype, cudaStream_t s);
+// In chunks of 64 tokens (delta_chunk.cu): bf16 storage, any strides, with a workspace of delta_chunk_workspace().
+size_t delta_chunk_workspace(int64_t B, int64_t L, int Hv);
+cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, cudaStream_t s);
 // One token, states in place (delta.cu).
 cudaError_t launch_delta_step(const DeltaArgs& a, int dtype, float* states, int64_t n_states, const int32_t* slots,
                               uint32_t* status, cudaStream_t s);

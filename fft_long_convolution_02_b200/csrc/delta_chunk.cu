@@ -1,0 +1,856 @@
+// delta_chunk.cu -- the gated delta rule over whole sequences in chunks of 64
+// tokens, bf16 storage.
+//
+// With G_i the sum of the log decays of the chunk's tokens up to i, the writes U
+// of a chunk solve a triangular system, and everything else is products:
+//   A_ij = beta_i e^{G_i - G_j} k_i.k_j  (j < i),     T = (1 + A)^-1 diag(beta)
+//   U  = T (V - diag(e^G) K S)
+//   O  = scale (diag(e^G) Q S + P U),    P_ij = e^{G_i - G_j} q_i.k_j  (j <= i)
+//   S <- e^{G_63} S + K^T diag(e^{G_63 - G_i}) U
+//
+// k_delta_prep: T, P and the factors of a chunk, all chunks at once, into the
+// workspace.  k_delta_scan: the chunks of a head in order, the state in
+// registers.
+//
+// Precision.  The state and what feeds it are held to fp32: K and Q are exact in
+// fp16 once a power of two brings a row's largest element to [2^13, 2^14)
+// (8 significant bits; what falls below 2^-37 of the row's largest is lost), and
+// S, T, V - .. and U go into the products as two fp16 parts each, 22 bits, under
+// such a power of two for each row (the low parts stay normal numbers down to
+// 2^-27 of the row's largest).  Sums are fp32.  The outputs are bf16, so on
+// their way S, P and U are one fp16 part each (11 bits).
+// e^{G_i - G_j} comes from sums held as two floats: their difference loses
+// nothing behind a strong decay.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "delta.h"
+#include "kernels.h"
+#include "tc_util.cuh"
+#include "tma_util.cuh"
+
+namespace hyena {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int C = 64;                              // tokens of a chunk
+
+// What k_delta_prep leaves for a chunk of a value head: T's two parts and P as
+// fp16 images of the scan's shared memory, and the factors of its 64 tokens.
+struct Factors {
+    float kmul[C], qmul[C];                        // K, Q rows to their fp16 range
+    float cx[C];                                   // (K S) row of the scaled K to diag(e^G) K S
+    float cu[C];                                   // U row to its part of the state
+    float co[C];                                   // (Q S) row of the scaled Q to the output
+    float cp[C], ct[C];                            // rows of the stored P and T to P and T
+    float gamma;                                   // e^{G_63}
+    float pad[63];
+};
+constexpr uint32_t kTile = C * C * 2;              // bytes of a 64 x 64 fp16 image
+constexpr uint32_t kBlob = 3 * kTile + uint32_t(sizeof(Factors));
+static_assert(sizeof(Factors) == 2048, "");
+
+// ------------------------------------------------------------------ fragments
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Shared-memory tiles of 16-bit numbers: rows of 16-byte pieces, piece c of row
+// r at c ^ (r mod 8), so that eight rows' pieces lie on different banks.
+template <int PIECES>
+__device__ __forceinline__ uint32_t piece(int row, int c) {
+    return uint32_t(row * PIECES + (c ^ (row & 7))) * 16u;
+}
+
+// The right operand (16 of k, 16 of n) from a tile stored [n][k] or [k][n]: r[0], r[1] serve the first 8 of n.
+template <int PIECES>
+__device__ __forceinline__ void right_nk(uint32_t (&r)[4], uint32_t tile, int k16, int n8, int lane) {
+    const int m = lane >> 3;
+    ldsm4(r, tile + piece<PIECES>(8 * (n8 + (m >> 1)) + (lane & 7), 2 * k16 + (m & 1)));
+}
+template <int PIECES>
+__device__ __forceinline__ void right_kn(uint32_t (&r)[4], uint32_t tile, int k16, int n8, int lane) {
+    const int m = lane >> 3;
+    ldsm4t(r, tile + piece<PIECES>(16 * k16 + 8 * (m & 1) + (lane & 7), n8 + (m >> 1)));
+}
+// The left operand (16 rows from 16 m16, 16 of k) from a tile stored [m][k] or [k][m].
+template <int PIECES>
+__device__ __forceinline__ void left_mk(uint32_t (&r)[4], uint32_t tile, int m16, int k16, int lane) {
+    const int m = lane >> 3;
+    ldsm4(r, tile + piece<PIECES>(16 * m16 + 8 * (m & 1) + (lane & 7), 2 * k16 + (m >> 1)));
+}
+template <int PIECES>
+__device__ __forceinline__ void left_km(uint32_t (&r)[4], uint32_t tile, int m16, int k16, int lane) {
+    const int m = lane >> 3;
+    ldsm4t(r, tile + piece<PIECES>(16 * k16 + 8 * (m >> 1) + (lane & 7), 2 * m16 + (m & 1)));
+}
+
+// The power of two that brings a largest magnitude m to [2^13, 2^14), and its
+// inverse; both normal numbers whatever m is.
+struct Pow2 {
+    float up, down;
+    __device__ __forceinline__ explicit Pow2(float m) {
+        int e = 267 - int(__float_as_uint(m) >> 23);
+        e = max(1, min(253, e));
+        up = __uint_as_float(uint32_t(e) << 23);
+        down = __uint_as_float(uint32_t(254 - e) << 23);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_h(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// a, b as fp16 pairs of a high and a low part
+__device__ __forceinline__ void split_h(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = pack_h(a - f.x, b - f.y);
+}
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+__device__ __forceinline__ float bf(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xffff0000u) : (w << 16)); }
+
+// Eight elements of a [channel, time] view from (c, t), along time (FIRST) or along channels; what lies outside
+// [0, nc) x [0, nt) is zero and not read.  vec: eight elements of a row inside the view are one aligned load.
+template <bool FIRST>
+__device__ __forceinline__ uint4 octet(const bf16* p, const DeltaView& s, int c, int t, int nc, int nt, bool vec) {
+    const bf16* at = p + int64_t(c) * s.sc + int64_t(t) * s.st;
+    const int n = FIRST ? (c < nc ? nt - t : 0) : (t < nt ? nc - c : 0);
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (n >= 8 && vec) return __ldg(reinterpret_cast<const uint4*>(at));
+    if (n > 0) {
+        const int64_t step = FIRST ? s.st : s.sc;
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = i < n ? uint32_t(__ldg(reinterpret_cast<const unsigned short*>(at + i * step))) : 0u;
+        w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+    return w;
+}
+
+struct ChunkArgs {
+    DeltaArgs a;
+    uint8_t* blobs;                                // [B][Hv][chunks][kBlob]
+    int chunks;
+    int vec_k, vec_q, vec_v, vec_o;                // rows may be read (written) 16 bytes at a time
+    uint64_t budget_ns;
+    uint32_t* status;
+};
+
+__device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
+    return a.lengths ? max(int64_t(0), min(a.L, int64_t(a.lengths[b]))) : a.L;
+}
+
+// ----------------------------------------------------------------------- prep
+// One CTA of four warps a chunk and value head.  K and Q as they are (bf16,
+// products exact in fp32) through mma.sync, warp w the 16 rows from 16 w, only
+// tiles on or under the diagonal.  The inverse of the unit triangle 1 + A in
+// fp32: the two 32 x 32 blocks on the diagonal by substitution (a thread a
+// column, the columns in registers), the block under them as -T22 (A21 T11).
+constexpr int kPrepThreads = 128;
+constexpr int kARow = 68;
+
+template <int DK, bool FIRST>
+struct PrepSmem {
+    static constexpr int kRows = FIRST ? DK : C, kPieces = FIRST ? 8 : DK / 8;
+    alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
+    alignas(16) float A[C][kARow], T[C][kARow];
+    float W[32][36];
+    float gh[C], gl[C], rk[C], rq[C], beta[C];
+    float part[2][4][C];
+};
+
+template <int DK, bool FIRST>
+__global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
+    using Sm = PrepSmem<DK, FIRST>;
+    constexpr int P = Sm::kPieces;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+    const DeltaArgs& a = x.a;
+    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int chunk = int(blockIdx.x), h = int(blockIdx.y);
+    const int64_t b = blockIdx.z, t0 = int64_t(chunk) * C;
+    const int64_t len = length_of(a, b);
+    if (t0 >= len) return;
+    const int n = int(min(int64_t(C), len - t0));
+    const int kh = h / (a.Hv / a.Hk);
+    const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc + t0 * a.ks.st;
+    const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc + t0 * a.qs.st;
+#pragma unroll
+    for (int i = tid; i < Sm::kRows * P; i += kPrepThreads) {
+        const int row = i / P, c = i % P;
+        const int ch = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
+        *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = octet<FIRST>(kp, a.ks, ch, tt, a.dk, n, x.vec_k);
+        *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n, x.vec_q);
+    }
+    // sums of the log decays as two floats (in double here), by the first warp: two tokens a lane
+    if (warp == 0) {
+        double v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = 2 * lane + j;
+            // -inf (empty the state) as a finite decay that underflows to 0 against everything
+            v[j] = (a.g && t < n) ? double(fmaxf(a.g[b * a.gs.sb + h * a.gs.sc + (t0 + t) * a.gs.st], -1e5f)) : 0.0;
+            if (a.g && t < n && isnan(a.g[b * a.gs.sb + h * a.gs.sc + (t0 + t) * a.gs.st])) v[j] = __longlong_as_double(0x7ff8000000000000ll);
+            sm.beta[t] = t < n ? (a.beta ? a.beta[b * a.bs.sb + h * a.bs.sc + (t0 + t) * a.bs.st] : 1.0f) : 0.0f;
+        }
+        double s = v[0] + v[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += o;
+        }
+        const double s0 = s - v[1];
+        sm.gh[2 * lane] = float(s0);
+        sm.gl[2 * lane] = float(s0 - double(float(s0)));
+        sm.gh[2 * lane + 1] = float(s);
+        sm.gl[2 * lane + 1] = float(s - double(float(s)));
+    }
+    __syncthreads();
+    // norms and largest elements of the rows: two threads a token, half of the channels each
+    {
+        const int t = tid & (C - 1), half = tid >> 6;
+        float k2 = 0.0f, q2 = 0.0f, km = 0.0f, qm = 0.0f;
+        if constexpr (FIRST) {
+#pragma unroll 8
+            for (int c = half * (DK / 2); c < (half + 1) * (DK / 2); ++c) {
+                const uint32_t at = piece<P>(c, t >> 3) + uint32_t(t & 7) * 2u;
+                const float kv = __bfloat162float(*reinterpret_cast<const bf16*>(sm.k + at));
+                const float qv = __bfloat162float(*reinterpret_cast<const bf16*>(sm.q + at));
+                k2 = fmaf(kv, kv, k2);
+                q2 = fmaf(qv, qv, q2);
+                km = fmaxf(km, fabsf(kv));
+                qm = fmaxf(qm, fabsf(qv));
+            }
+        } else {
+#pragma unroll
+            for (int c = half * (P / 2); c < (half + 1) * (P / 2); ++c) {
+                const uint4 kw = *reinterpret_cast<const uint4*>(sm.k + piece<P>(t, c));
+                const uint4 qw = *reinterpret_cast<const uint4*>(sm.q + piece<P>(t, c));
+                const uint32_t ku[4] = {kw.x, kw.y, kw.z, kw.w}, qu[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float kv = bf(ku[i >> 1], i & 1), qv = bf(qu[i >> 1], i & 1);
+                    k2 = fmaf(kv, kv, k2);
+                    q2 = fmaf(qv, qv, q2);
+                    km = fmaxf(km, fabsf(kv));
+                    qm = fmaxf(qm, fabsf(qv));
+                }
+            }
+        }
+        sm.part[half][0][t] = k2;
+        sm.part[half][1][t] = q2;
+        sm.part[half][2][t] = km;
+        sm.part[half][3][t] = qm;
+    }
+    __syncthreads();
+    uint8_t* blob = x.blobs + ((b * a.Hv + h) * int64_t(x.chunks) + chunk) * kBlob;
+    Factors* f = reinterpret_cast<Factors*>(blob + 3 * kTile);
+    if (tid < C) {
+        const int t = tid;
+        const float rk = a.l2norm ? 1.0f / sqrtf(sm.part[0][0][t] + sm.part[1][0][t] + kDeltaNormEps) : 1.0f;
+        const float rq = (a.l2norm ? 1.0f / sqrtf(sm.part[0][1][t] + sm.part[1][1][t] + kDeltaNormEps) : 1.0f) * a.scale;
+        sm.rk[t] = rk;
+        sm.rq[t] = rq;
+        const Pow2 pk(fmaxf(sm.part[0][2][t], sm.part[1][2][t])), pq(fmaxf(sm.part[0][3][t], sm.part[1][3][t]));
+        const float into = expf(sm.gh[t] + sm.gl[t]);
+        const float out = expf((sm.gh[C - 1] - sm.gh[t]) + (sm.gl[C - 1] - sm.gl[t]));
+        f->kmul[t] = pk.up;
+        f->qmul[t] = pq.up;
+        f->cx[t] = into * rk * pk.down;
+        f->cu[t] = out * rk * pk.down;
+        f->co[t] = into * rq * pq.down;
+        if (t == 0) f->gamma = expf(sm.gh[C - 1] + sm.gl[C - 1]);
+    }
+    // K K^T and Q K^T, rows 16 warp ..
+    const uint32_t tk = tc::smem_u32(sm.k), tq = tc::smem_u32(sm.q);
+    float ka[8][4], qa[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ka[i][j] = qa[i][j] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t lk[4], lq[4];
+        if constexpr (FIRST) {
+            left_km<P>(lk, tk, warp, ks, lane);
+            left_km<P>(lq, tq, warp, ks, lane);
+        } else {
+            left_mk<P>(lk, tk, warp, ks, lane);
+            left_mk<P>(lq, tq, warp, ks, lane);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; nt += 2) {
+            if (nt > 2 * warp) break;
+            uint32_t r[4];
+            if constexpr (FIRST) right_kn<P>(r, tk, ks, nt, lane);
+            else right_nk<P>(r, tk, ks, nt, lane);
+            mma_bf16(ka[nt], lk, r[0], r[1]);
+            mma_bf16(ka[nt + 1], lk, r[2], r[3]);
+            mma_bf16(qa[nt], lq, r[0], r[1]);
+            mma_bf16(qa[nt + 1], lq, r[2], r[3]);
+        }
+    }
+    __syncthreads();                               // rk, rq
+    float pm[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 16 * warp + g + 8 * (j >> 1), c = 8 * nt + 2 * t4 + (j & 1);
+            const float d = c <= r ? expf((sm.gh[r] - sm.gh[c]) + (sm.gl[r] - sm.gl[c])) * sm.rk[c] : 0.0f;
+            sm.A[r][c] = c < r ? sm.beta[r] * sm.rk[r] * d * ka[nt][j] : 0.0f;
+            qa[nt][j] = c <= r ? d * sm.rq[r] * qa[nt][j] : 0.0f;
+            pm[j >> 1] = fmaxf(pm[j >> 1], fabsf(qa[nt][j]));
+        }
+    const Pow2 p0(quad_max(pm[0])), p1(quad_max(pm[1]));
+    if (t4 == 0) {
+        f->cp[16 * warp + g] = p0.down;
+        f->cp[16 * warp + g + 8] = p1.down;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        uint8_t* P2 = blob + 2 * kTile + 4 * t4;
+        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g, nt)) = pack_h(qa[nt][0] * p0.up, qa[nt][1] * p0.up);
+        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g + 8, nt)) = pack_h(qa[nt][2] * p1.up, qa[nt][3] * p1.up);
+    }
+    __syncthreads();
+    if (warp < 2) {
+        const int o = 32 * warp;
+        float xx[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            float s0 = i == lane ? 1.0f : 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; j += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(&sm.A[o + i][o + j]);
+                s0 = fmaf(-w.x, xx[j], s0);
+                if (j + 1 < i) s1 = fmaf(-w.y, xx[j + 1], s1);
+                if (j + 2 < i) s0 = fmaf(-w.z, xx[j + 2], s0);
+                if (j + 3 < i) s1 = fmaf(-w.w, xx[j + 3], s1);
+            }
+            xx[i] = s0 + s1;
+            sm.T[o + i][o + lane] = xx[i];
+        }
+    }
+    __syncthreads();
+    {
+        const int r = tid >> 2, c = (tid & 3) * 8;
+        float acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float w = sm.A[32 + r][k];
+            const float4 u = *reinterpret_cast<const float4*>(&sm.T[k][c]), v = *reinterpret_cast<const float4*>(&sm.T[k][c + 4]);
+            acc[0] = fmaf(w, u.x, acc[0]); acc[1] = fmaf(w, u.y, acc[1]); acc[2] = fmaf(w, u.z, acc[2]); acc[3] = fmaf(w, u.w, acc[3]);
+            acc[4] = fmaf(w, v.x, acc[4]); acc[5] = fmaf(w, v.y, acc[5]); acc[6] = fmaf(w, v.z, acc[6]); acc[7] = fmaf(w, v.w, acc[7]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sm.W[r][c + i] = acc[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float w = -sm.T[32 + r][32 + k];
+            const float4 u = *reinterpret_cast<const float4*>(&sm.W[k][c]), v = *reinterpret_cast<const float4*>(&sm.W[k][c + 4]);
+            acc[0] = fmaf(w, u.x, acc[0]); acc[1] = fmaf(w, u.y, acc[1]); acc[2] = fmaf(w, u.z, acc[2]); acc[3] = fmaf(w, u.w, acc[3]);
+            acc[4] = fmaf(w, v.x, acc[4]); acc[5] = fmaf(w, v.y, acc[5]); acc[6] = fmaf(w, v.z, acc[6]); acc[7] = fmaf(w, v.w, acc[7]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sm.T[32 + r][c + i] = acc[i];
+    }
+    __syncthreads();
+    // T diag(beta) in two parts: two threads a row, half of the columns each
+    {
+        const int r = tid >> 1, c0 = (tid & 1) * 32;
+        float m = 0.0f;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[i] = c0 + i <= r ? sm.T[r][c0 + i] * sm.beta[c0 + i] : 0.0f;
+            m = fmaxf(m, fabsf(v[i]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const Pow2 p(m);
+        if (c0 == 0) f->ct[r] = p.down;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split_h(v[8 * i + 2 * j] * p.up, v[8 * i + 2 * j + 1] * p.up, hi[j], lo[j]);
+            const uint32_t at = piece<8>(r, c0 / 8 + i);
+            *reinterpret_cast<uint4*>(blob + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(blob + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+}
+
+// ----------------------------------------------------------------------- scan
+// A CTA takes 16 NW value channels of a head: NW warps of 16 channels each (the
+// channels never mix) and four loading warps.  A warp works on the transposes,
+// S^T [16 x DK] in accumulators: each product's result is the next one's left
+// operand as it lies in registers,
+//   X^T = S^T K^T,  R^T = V^T - X^T diag(cx),  U^T = R^T T^T,  S^T += U^T diag(cu) K,
+// so a chunk's chain has no shared-memory round trip and no barrier.  The
+// loaders bring K and Q to fp16 under their powers of two, V as it is, and T, P
+// and the factors as one bulk copy, two chunks deep.
+// mma.sync, not tcgen05: the chain's four dependent products take registers to
+// registers here, and a CTA's 16 x 64 operands are below tcgen05's 128 rows.
+constexpr int kLoaders = 128;
+constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
+
+template <int DK, int NW>
+struct ScanSmem {
+    struct Stage {
+        alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
+        alignas(128) uint8_t blob[kBlob];          // T high, T low, P, factors
+        alignas(16) bf16 v[16 * NW][kVRow];
+    } st[2];
+    alignas(16) bf16 o[NW][16 * kVRow];            // [channel][time], or [time][16 + 8]
+    uint64_t full[2], empty[2];
+};
+
+__device__ __forceinline__ uint4 scaled8(const uint4& w, const float (&m)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack_h(bf(u[i], 0) * m[2 * i], bf(u[i], 1) * m[2 * i + 1]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int DK, int NW, bool FIRST>
+__global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs x) {
+    using Sm = ScanSmem<DK, NW>;
+    constexpr int P = FIRST ? 8 : DK / 8;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+    const DeltaArgs& a = x.a;
+    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int h = int(blockIdx.y), d0 = int(blockIdx.x) * 16 * NW;
+    const int64_t b = blockIdx.z;
+    const int64_t len = length_of(a, b);
+    const int chunks = int((len + C - 1) / C);
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&sm.full[s], kLoaders + 1);
+            tc::mbar_init(&sm.empty[s], NW);
+        }
+    }
+    __syncthreads();
+    if (warp >= NW) {
+        // ------------------------------------------------------------ loaders
+        // registers of eight warps: 384 x 168 at launch = 128 x 56 + 256 x 224
+        if constexpr (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        const int lt = tid - 32 * NW;
+        const int kh = h / (a.Hv / a.Hk);
+        const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc;
+        const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc;
+        const bf16* vp = static_cast<const bf16*>(a.v) + b * a.vs.sb + (int64_t(h) * a.dv + d0) * a.vs.sc;
+        const uint8_t* blobs = x.blobs + (b * a.Hv + h) * int64_t(x.chunks) * kBlob;
+        const int cols = min(16 * NW, a.dv - d0);
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int s = ch & 1;
+            typename Sm::Stage& st = sm.st[s];
+            if (!tc::mbar_wait(&sm.empty[s], (uint32_t(ch >> 1) & 1u) ^ 1u, x.budget_ns)) {
+                if (lane == 0) report_status(x.status, kStatusTimeout);
+                break;
+            }
+            const uint8_t* blob = blobs + int64_t(ch) * kBlob;
+            if (lt == 0) {
+                tc::mbar_expect_tx(&sm.full[s], kBlob);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                                 tc::smem_u32(st.blob)), "l"(blob), "r"(kBlob), "r"(tc::smem_u32(&sm.full[s]))
+                             : "memory");
+            }
+            const int64_t t0 = int64_t(ch) * C;
+            const int n = int(min(int64_t(C), len - t0));
+            const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
+            constexpr int kRows = FIRST ? DK : C;
+            float mk[8], mq[8];
+            if constexpr (FIRST) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {      // this thread's eight tokens
+                    mk[i] = f->kmul[8 * (lt % 8) + i];
+                    mq[i] = f->qmul[8 * (lt % 8) + i];
+                }
+            }
+#pragma unroll 4
+            for (int i = lt; i < kRows * P; i += kLoaders) {
+                const int row = i / P, c = i % P;
+                const int chn = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
+                const uint4 kw = octet<FIRST>(kp + t0 * a.ks.st, a.ks, chn, tt, a.dk, n, x.vec_k);
+                const uint4 qw = octet<FIRST>(qp + t0 * a.qs.st, a.qs, chn, tt, a.dk, n, x.vec_q);
+                if constexpr (!FIRST) {
+                    const float k1 = f->kmul[row], q1 = f->qmul[row];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        mk[j] = k1;
+                        mq[j] = q1;
+                    }
+                }
+                *reinterpret_cast<uint4*>(st.k + piece<P>(row, c)) = scaled8(kw, mk);
+                *reinterpret_cast<uint4*>(st.q + piece<P>(row, c)) = scaled8(qw, mq);
+            }
+            if constexpr (FIRST) {
+#pragma unroll 4
+                for (int i = lt; i < 16 * NW * 8; i += kLoaders) {
+                    const int row = i / 8, c = i % 8;
+                    *reinterpret_cast<uint4*>(&st.v[row][8 * c]) = octet<true>(vp + t0 * a.vs.st, a.vs, row, 8 * c, cols, n, x.vec_v);
+                }
+            } else {
+                // eight channels of two tokens each way: pairs of tokens lie together in V^T
+#pragma unroll 2
+                for (int i = lt; i < 32 * 2 * NW; i += kLoaders) {
+                    const int tp = i % 32, c = i / 32;
+                    const uint4 w0 = octet<false>(vp + t0 * a.vs.st, a.vs, 8 * c, 2 * tp, cols, n, x.vec_v);
+                    const uint4 w1 = octet<false>(vp + t0 * a.vs.st, a.vs, 8 * c, 2 * tp + 1, cols, n, x.vec_v);
+                    const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint32_t*>(&st.v[8 * c + j][2 * tp]) =
+                            __byte_perm(u0[j >> 1], u1[j >> 1], (j & 1) ? 0x7632 : 0x5410);
+                }
+            }
+            tc::mbar_arrive(&sm.full[s]);
+        }
+        // the last copies have landed before the CTA may end: the scanning warps wait for every stage
+        return;
+    }
+    // ------------------------------------------------------------------- scan
+    if constexpr (NW == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+    const int g = lane >> 2, t4 = lane & 3;
+    const int dw = d0 + 16 * warp;                 // this warp's first channel
+    const int64_t sb = (b * a.Hv + h) * int64_t(a.dk) * a.dv;
+    float S[DK / 8][4];
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = dw + g + 8 * (i >> 1), r = 8 * j + 2 * t4 + (i & 1);
+            S[j][i] = (a.state_in && d < a.dv && r < a.dk) ? a.state_in[sb + int64_t(r) * a.dv + d] : 0.0f;
+        }
+    bf16* ob = static_cast<bf16*>(a.o) + b * a.os.sb + (int64_t(h) * a.dv + dw) * a.os.sc;
+    bf16* so = sm.o[warp];
+    for (int ch = 0; ch < chunks; ++ch) {
+        const int s = ch & 1;
+        typename Sm::Stage& st = sm.st[s];
+        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) {
+            if (lane == 0) report_status(x.status, kStatusTimeout);
+#pragma unroll
+            for (int j = 0; j < DK / 8; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
+            break;
+        }
+        const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
+        const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
+        float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j) {
+            m0 = fmaxf(m0, fmaxf(fabsf(S[j][0]), fabsf(S[j][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(S[j][2]), fabsf(S[j][3])));
+        }
+        const Pow2 ps0(quad_max(m0)), ps1(quad_max(m1));
+        float X[8][4], O[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) X[i][j] = O[i][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                split_h(S[2 * ks + j][0] * ps0.up, S[2 * ks + j][1] * ps0.up, hi[2 * j], lo[2 * j]);
+                split_h(S[2 * ks + j][2] * ps1.up, S[2 * ks + j][3] * ps1.up, hi[2 * j + 1], lo[2 * j + 1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; nt += 2) {
+                uint32_t r[4], w[4];
+                if constexpr (FIRST) {
+                    right_kn<P>(r, tk, ks, nt, lane);
+                    right_kn<P>(w, tq, ks, nt, lane);
+                } else {
+                    right_nk<P>(r, tk, ks, nt, lane);
+                    right_nk<P>(w, tq, ks, nt, lane);
+                }
+                mma_f16(X[nt], hi, r[0], r[1]);
+                mma_f16(X[nt + 1], hi, r[2], r[3]);
+                mma_f16(O[nt], hi, w[0], w[1]);
+                mma_f16(O[nt + 1], hi, w[2], w[3]);
+                mma_f16(X[nt], lo, r[0], r[1]);
+                mma_f16(X[nt + 1], lo, r[2], r[3]);
+            }
+        }
+        // R^T = V^T - X^T diag(cx); the outputs' part of the state
+        m0 = m1 = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const int t = 8 * nt + 2 * t4;
+            const float2 cx = *reinterpret_cast<const float2*>(&f.cx[t]), co = *reinterpret_cast<const float2*>(&f.co[t]);
+            const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&st.v[16 * warp + g][t]);
+            const uint32_t v1 = *reinterpret_cast<const uint32_t*>(&st.v[16 * warp + g + 8][t]);
+            X[nt][0] = fmaf(-X[nt][0] * ps0.down, cx.x, bf(v0, 0));
+            X[nt][1] = fmaf(-X[nt][1] * ps0.down, cx.y, bf(v0, 1));
+            X[nt][2] = fmaf(-X[nt][2] * ps1.down, cx.x, bf(v1, 0));
+            X[nt][3] = fmaf(-X[nt][3] * ps1.down, cx.y, bf(v1, 1));
+            m0 = fmaxf(m0, fmaxf(fabsf(X[nt][0]), fabsf(X[nt][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(X[nt][2]), fabsf(X[nt][3])));
+            O[nt][0] = O[nt][0] * ps0.down * co.x;
+            O[nt][1] = O[nt][1] * ps0.down * co.y;
+            O[nt][2] = O[nt][2] * ps1.down * co.x;
+            O[nt][3] = O[nt][3] * ps1.down * co.y;
+        }
+        const Pow2 pr0(quad_max(m0)), pr1(quad_max(m1));
+        // U^T = R^T T^T, tiles on and right of the diagonal
+        float U[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) U[i][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                split_h(X[2 * ks + j][0] * pr0.up, X[2 * ks + j][1] * pr0.up, hi[2 * j], lo[2 * j]);
+                split_h(X[2 * ks + j][2] * pr1.up, X[2 * ks + j][3] * pr1.up, hi[2 * j + 1], lo[2 * j + 1]);
+            }
+#pragma unroll
+            for (int nt = 2 * ks; nt < 8; nt += 2) {
+                uint32_t r[4], w[4];
+                right_nk<8>(r, tb, ks, nt, lane);
+                right_nk<8>(w, tb + kTile, ks, nt, lane);
+                mma_f16(U[nt], hi, r[0], r[1]);
+                mma_f16(U[nt + 1], hi, r[2], r[3]);
+                mma_f16(U[nt], lo, r[0], r[1]);
+                mma_f16(U[nt + 1], lo, r[2], r[3]);
+                mma_f16(U[nt], hi, w[0], w[1]);
+                mma_f16(U[nt + 1], hi, w[2], w[3]);
+            }
+        }
+        m0 = m1 = 0.0f;
+        float n0 = 0.0f, n1 = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const int t = 8 * nt + 2 * t4;
+            const float2 ct = *reinterpret_cast<const float2*>(&f.ct[t]), cu = *reinterpret_cast<const float2*>(&f.cu[t]);
+            U[nt][0] = U[nt][0] * pr0.down * ct.x;
+            U[nt][1] = U[nt][1] * pr0.down * ct.y;
+            U[nt][2] = U[nt][2] * pr1.down * ct.x;
+            U[nt][3] = U[nt][3] * pr1.down * ct.y;
+            m0 = fmaxf(m0, fmaxf(fabsf(U[nt][0]), fabsf(U[nt][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(U[nt][2]), fabsf(U[nt][3])));
+            X[nt][0] = U[nt][0] * cu.x;
+            X[nt][1] = U[nt][1] * cu.y;
+            X[nt][2] = U[nt][2] * cu.x;
+            X[nt][3] = U[nt][3] * cu.y;
+            n0 = fmaxf(n0, fmaxf(fabsf(X[nt][0]), fabsf(X[nt][1])));
+            n1 = fmaxf(n1, fmaxf(fabsf(X[nt][2]), fabsf(X[nt][3])));
+        }
+        const Pow2 pu0(quad_max(m0)), pu1(quad_max(m1)), pw0(quad_max(n0)), pw1(quad_max(n1));
+        // S^T = gamma S^T + (U diag(cu))^T K
+        uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                split_h(X[2 * ks + j][0] * pw0.up, X[2 * ks + j][1] * pw0.up, hi[ks][2 * j], lo[ks][2 * j]);
+                split_h(X[2 * ks + j][2] * pw1.up, X[2 * ks + j][3] * pw1.up, hi[ks][2 * j + 1], lo[ks][2 * j + 1]);
+            }
+        const float gamma = f.gamma;
+#pragma unroll
+        for (int nt = 0; nt < DK / 8; nt += 4) {
+            float D[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) D[i][j] = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t r[4], w[4];
+                if constexpr (FIRST) {
+                    right_nk<P>(r, tk, ks, nt, lane);
+                    right_nk<P>(w, tk, ks, nt + 2, lane);
+                } else {
+                    right_kn<P>(r, tk, ks, nt, lane);
+                    right_kn<P>(w, tk, ks, nt + 2, lane);
+                }
+                mma_f16(D[0], hi[ks], r[0], r[1]);
+                mma_f16(D[1], hi[ks], r[2], r[3]);
+                mma_f16(D[2], hi[ks], w[0], w[1]);
+                mma_f16(D[3], hi[ks], w[2], w[3]);
+                mma_f16(D[0], lo[ks], r[0], r[1]);
+                mma_f16(D[1], lo[ks], r[2], r[3]);
+                mma_f16(D[2], lo[ks], w[0], w[1]);
+                mma_f16(D[3], lo[ks], w[2], w[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[nt + i][0] = fmaf(gamma, S[nt + i][0], D[i][0] * pw0.down);
+                S[nt + i][1] = fmaf(gamma, S[nt + i][1], D[i][1] * pw0.down);
+                S[nt + i][2] = fmaf(gamma, S[nt + i][2], D[i][2] * pw1.down);
+                S[nt + i][3] = fmaf(gamma, S[nt + i][3], D[i][3] * pw1.down);
+            }
+        }
+        // O^T += U^T P^T
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                u[2 * j] = pack_h(U[2 * ks + j][0] * pu0.up, U[2 * ks + j][1] * pu0.up);
+                u[2 * j + 1] = pack_h(U[2 * ks + j][2] * pu1.up, U[2 * ks + j][3] * pu1.up);
+            }
+#pragma unroll
+            for (int nt = 2 * ks; nt < 8; nt += 2) {
+                uint32_t r[4];
+                right_nk<8>(r, tb + 2 * kTile, ks, nt, lane);
+                mma_f16(X[nt], u, r[0], r[1]);
+                mma_f16(X[nt + 1], u, r[2], r[3]);
+            }
+        }
+        // out through shared memory: whole rows leave
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const int t = 8 * nt + 2 * t4;
+            const float2 cp = *reinterpret_cast<const float2*>(&f.cp[t]);
+            const __nv_bfloat162 y0 = __floats2bfloat162_rn(fmaf(X[nt][0] * pu0.down, cp.x, O[nt][0]), fmaf(X[nt][1] * pu0.down, cp.y, O[nt][1]));
+            const __nv_bfloat162 y1 = __floats2bfloat162_rn(fmaf(X[nt][2] * pu1.down, cp.x, O[nt][2]), fmaf(X[nt][3] * pu1.down, cp.y, O[nt][3]));
+            if constexpr (FIRST) {
+                *reinterpret_cast<__nv_bfloat162*>(so + g * kVRow + t) = y0;
+                *reinterpret_cast<__nv_bfloat162*>(so + (g + 8) * kVRow + t) = y1;
+            } else {
+                so[t * 16 + g] = y0.x;
+                so[(t + 1) * 16 + g] = y0.y;
+                so[t * 16 + g + 8] = y1.x;
+                so[(t + 1) * 16 + g + 8] = y1.y;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+        const int64_t t0 = int64_t(ch) * C;
+        const int n = int(min(int64_t(C), len - t0)), cols = min(16, a.dv - dw);
+        bf16* oc = ob + t0 * a.os.st;
+        if constexpr (FIRST) {
+#pragma unroll
+            for (int i = lane; i < 16 * 8; i += 32) {
+                const int r = i >> 3, t = (i & 7) * 8;
+                if (r >= cols) continue;
+                if (x.vec_o && t + 8 <= n) {
+                    *reinterpret_cast<uint4*>(oc + int64_t(r) * a.os.sc + t) = *reinterpret_cast<const uint4*>(so + r * kVRow + t);
+                } else {
+                    for (int j = 0; j < 8 && t + j < n; ++j) oc[int64_t(r) * a.os.sc + int64_t(t + j) * a.os.st] = so[r * kVRow + t + j];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = lane; i < C * 2; i += 32) {
+                const int t = i >> 1, c = (i & 1) * 8;
+                if (t >= n) continue;
+                if (x.vec_o && c + 8 <= cols) {
+                    *reinterpret_cast<uint4*>(oc + int64_t(t) * a.os.st + c) = *reinterpret_cast<const uint4*>(so + t * 16 + c);
+                } else {
+                    for (int j = 0; j < 8 && c + j < cols; ++j) oc[int64_t(t) * a.os.st + int64_t(c + j) * a.os.sc] = so[t * 16 + c + j];
+                }
+            }
+        }
+        __syncwarp();
+    }
+    if (a.state_out) {
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = dw + g + 8 * (i >> 1), r = 8 * j + 2 * t4 + (i & 1);
+                if (d < a.dv && r < a.dk) a.state_out[sb + int64_t(r) * a.dv + d] = S[j][i];
+            }
+    }
+}
+
+// --------------------------------------------------------------------- host
+// Eight elements along the contiguous axis as one 16-byte access, wherever a row starts.
+bool vec_ok(const void* p, const DeltaView& s, bool first, int head_channels) {
+    const int64_t row = first ? s.sc : s.st;
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (first ? s.st : s.sc) == 1 && row % 8 == 0 && s.sb % 8 == 0 &&
+           (first || head_channels % 8 == 0);
+}
+
+template <int DK, bool FIRST>
+cudaError_t launch_prep(const ChunkArgs& x, cudaStream_t s) {
+    const size_t bytes = sizeof(PrepSmem<DK, FIRST>);
+    cudaError_t e = cudaFuncSetAttribute(k_delta_prep<DK, FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    k_delta_prep<DK, FIRST><<<dim3(unsigned(x.chunks), unsigned(x.a.Hv), unsigned(x.a.B)), kPrepThreads, bytes, s>>>(x);
+    return cudaGetLastError();
+}
+
+template <int DK, int NW, bool FIRST>
+cudaError_t launch_scan(const ChunkArgs& x, cudaStream_t s) {
+    const size_t bytes = sizeof(ScanSmem<DK, NW>);
+    cudaError_t e = cudaFuncSetAttribute(k_delta_scan<DK, NW, FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    const dim3 grid(unsigned((x.a.dv + 16 * NW - 1) / (16 * NW)), unsigned(x.a.Hv), unsigned(x.a.B));
+    k_delta_scan<DK, NW, FIRST><<<grid, 32 * NW + kLoaders, bytes, s>>>(x);
+    return cudaGetLastError();
+}
+
+template <int DK, bool FIRST>
+cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
+    cudaError_t e = launch_prep<DK, FIRST>(x, s);
+    if (e != cudaSuccess) return e;
+    // four warps have a scheduler each; eight share them, which pays once half-width CTAs would not all be resident
+    const int64_t ctas = x.a.B * x.a.Hv * ((x.a.dv + 63) / 64);
+    return ctas <= 148 ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
+}
+
+}  // namespace
+
+size_t delta_chunk_workspace(int64_t B, int64_t L, int Hv) { return size_t(B) * size_t(Hv) * size_t((L + C - 1) / C) * kBlob; }
+
+cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, cudaStream_t s) {
+    ChunkArgs x{};
+    x.a = a;
+    x.blobs = static_cast<uint8_t*>(workspace);
+    x.chunks = int((a.L + C - 1) / C);
+    x.budget_ns = kDefaultWaitBudgetNs;
+    x.status = status;
+    // the tiles lie as the keys do: along time where that is their contiguous axis
+    const bool first = a.ks.st == 1 || a.ks.sc != 1;
+    x.vec_k = vec_ok(a.k, a.ks, first, a.dk);
+    x.vec_q = vec_ok(a.q, a.qs, first, a.dk);
+    x.vec_v = vec_ok(a.v, a.vs, first, a.dv);
+    x.vec_o = vec_ok(a.o, a.os, first, a.dv);
+    if (a.dk <= 64) return first ? launch_both<64, true>(x, s) : launch_both<64, false>(x, s);
+    return first ? launch_both<128, true>(x, s) : launch_both<128, false>(x, s);
+}
+
+}  // namespace hyena
