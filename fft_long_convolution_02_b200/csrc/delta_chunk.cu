@@ -152,6 +152,17 @@ __device__ __forceinline__ uint4 octet(const bf16* p, const DeltaView& s, int c,
     return w;
 }
 
+// Whether all octets of a [nc] x [nt] tile lie inside it or outside it as wholes, and load as such: then a thread's
+// loads go out together (octet()'s piecewise path would put each behind the one before).
+template <bool FIRST>
+__device__ __forceinline__ bool whole(int nc, int nt, bool vec) {
+    return vec && ((FIRST ? nt : nc) & 7) == 0;
+}
+template <bool FIRST>
+__device__ __forceinline__ uint4 whole_octet(const bf16* p, const DeltaView& s, int c, int t, int nc, int nt) {
+    return c < nc && t < nt ? __ldg(reinterpret_cast<const uint4*>(p + int64_t(c) * s.sc + int64_t(t) * s.st)) : make_uint4(0, 0, 0, 0);
+}
+
 struct ChunkArgs {
     DeltaArgs a;
     uint8_t* blobs;                                // [B][Hv][chunks][kBlob]
@@ -200,12 +211,29 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
     const int kh = h / (a.Hv / a.Hk);
     const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc + t0 * a.ks.st;
     const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc + t0 * a.qs.st;
+    constexpr int kOct = Sm::kRows * P / kPrepThreads;
+    if (whole<FIRST>(a.dk, n, x.vec_k && x.vec_q)) {
+        uint4 w[2][kOct];
 #pragma unroll
-    for (int i = tid; i < Sm::kRows * P; i += kPrepThreads) {
-        const int row = i / P, c = i % P;
-        const int ch = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
-        *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = octet<FIRST>(kp, a.ks, ch, tt, a.dk, n, x.vec_k);
-        *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n, x.vec_q);
+        for (int j = 0; j < kOct; ++j) {
+            const int row = (tid + j * kPrepThreads) / P, c = (tid + j * kPrepThreads) % P;
+            w[0][j] = whole_octet<FIRST>(kp, a.ks, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
+            w[1][j] = whole_octet<FIRST>(qp, a.qs, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
+        }
+#pragma unroll
+        for (int j = 0; j < kOct; ++j) {
+            const int row = (tid + j * kPrepThreads) / P, c = (tid + j * kPrepThreads) % P;
+            *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = w[0][j];
+            *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = w[1][j];
+        }
+    } else {
+#pragma unroll 1
+        for (int i = tid; i < Sm::kRows * P; i += kPrepThreads) {
+            const int row = i / P, c = i % P;
+            const int ch = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
+            *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = octet<FIRST>(kp, a.ks, ch, tt, a.dk, n, x.vec_k);
+            *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n, x.vec_q);
+        }
     }
     // sums of the log decays as two floats (in double here), by the first warp: two tokens a lane
     if (warp == 0) {
@@ -444,6 +472,83 @@ __device__ __forceinline__ uint4 scaled8(const uint4& w, const float (&m)[8]) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// A K or Q tile to fp16 under the tokens' powers of two: m holds those of this thread's eight tokens (FIRST), mul
+// those of all.
+template <int DK, bool FIRST>
+__device__ __forceinline__ void load_scaled(uint8_t* tile, const bf16* p, const DeltaView& s, const float (&m)[8],
+                                            const float* mul, int dk, int n, bool vec, int lt) {
+    constexpr int P = FIRST ? 8 : DK / 8, kOct = C * DK / 8 / kLoaders;
+    auto put = [&](int i, const uint4& w) {
+        const int row = i / P, c = i % P;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = FIRST ? m[j] : mul[row];
+        *reinterpret_cast<uint4*>(tile + piece<P>(row, c)) = scaled8(w, f);
+    };
+    if (whole<FIRST>(dk, n, vec)) {
+        uint4 w[kOct];
+#pragma unroll
+        for (int j = 0; j < kOct; ++j) {
+            const int row = (lt + j * kLoaders) / P, c = (lt + j * kLoaders) % P;
+            w[j] = whole_octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n);
+        }
+#pragma unroll
+        for (int j = 0; j < kOct; ++j) put(lt + j * kLoaders, w[j]);
+    } else {
+#pragma unroll 1
+        for (int i = lt; i < C * DK / 8; i += kLoaders) {
+            const int row = i / P, c = i % P;
+            put(i, octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n, vec));
+        }
+    }
+}
+
+// V^T [16 NW][kVRow]; from tokens' rows (not FIRST) eight channels of two tokens each way, as pairs of tokens lie together.
+template <int NW, bool FIRST>
+__device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf16* p, const DeltaView& s, int cols, int n,
+                                            bool vec, int lt) {
+    constexpr int kOct = 16 * NW * 8 / kLoaders;
+    if constexpr (FIRST) {
+        auto put = [&](int i, const uint4& w) { *reinterpret_cast<uint4*>(&v[i / 8][8 * (i % 8)]) = w; };
+        if (whole<true>(cols, n, vec)) {
+            uint4 w[kOct];
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) w[j] = whole_octet<true>(p, s, (lt + j * kLoaders) / 8, 8 * ((lt + j * kLoaders) % 8), cols, n);
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) put(lt + j * kLoaders, w[j]);
+        } else {
+#pragma unroll 1
+            for (int i = lt; i < 16 * NW * 8; i += kLoaders) put(i, octet<true>(p, s, i / 8, 8 * (i % 8), cols, n, vec));
+        }
+    } else {
+        // neighbouring lanes: neighbouring octets of a token's row, so whole sectors are read
+        constexpr int kRowOct = 2 * NW;
+        auto put = [&](int i, const uint4& w0, const uint4& w1) {
+            const int tp = i / kRowOct, c = i % kRowOct;
+            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint32_t*>(&v[8 * c + j][2 * tp]) = __byte_perm(u0[j >> 1], u1[j >> 1], (j & 1) ? 0x7632 : 0x5410);
+        };
+        if (whole<false>(cols, n, vec)) {
+            uint4 w[kOct];
+#pragma unroll
+            for (int j = 0; j < kOct / 2; ++j) {
+                const int i = lt + j * kLoaders;
+                w[2 * j] = whole_octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct), cols, n);
+                w[2 * j + 1] = whole_octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct) + 1, cols, n);
+            }
+#pragma unroll
+            for (int j = 0; j < kOct / 2; ++j) put(lt + j * kLoaders, w[2 * j], w[2 * j + 1]);
+        } else {
+#pragma unroll 1
+            for (int i = lt; i < 32 * kRowOct; i += kLoaders)
+                put(i, octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct), cols, n, vec),
+                    octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct) + 1, cols, n, vec));
+        }
+    }
+}
+
 template <int DK, int NW, bool FIRST>
 __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs x) {
     using Sm = ScanSmem<DK, NW>;
@@ -491,7 +596,6 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             const int64_t t0 = int64_t(ch) * C;
             const int n = int(min(int64_t(C), len - t0));
             const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
-            constexpr int kRows = FIRST ? DK : C;
             float mk[8], mq[8];
             if constexpr (FIRST) {
 #pragma unroll
@@ -500,43 +604,9 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
                     mq[i] = f->qmul[8 * (lt % 8) + i];
                 }
             }
-#pragma unroll 4
-            for (int i = lt; i < kRows * P; i += kLoaders) {
-                const int row = i / P, c = i % P;
-                const int chn = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
-                const uint4 kw = octet<FIRST>(kp + t0 * a.ks.st, a.ks, chn, tt, a.dk, n, x.vec_k);
-                const uint4 qw = octet<FIRST>(qp + t0 * a.qs.st, a.qs, chn, tt, a.dk, n, x.vec_q);
-                if constexpr (!FIRST) {
-                    const float k1 = f->kmul[row], q1 = f->qmul[row];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        mk[j] = k1;
-                        mq[j] = q1;
-                    }
-                }
-                *reinterpret_cast<uint4*>(st.k + piece<P>(row, c)) = scaled8(kw, mk);
-                *reinterpret_cast<uint4*>(st.q + piece<P>(row, c)) = scaled8(qw, mq);
-            }
-            if constexpr (FIRST) {
-#pragma unroll 4
-                for (int i = lt; i < 16 * NW * 8; i += kLoaders) {
-                    const int row = i / 8, c = i % 8;
-                    *reinterpret_cast<uint4*>(&st.v[row][8 * c]) = octet<true>(vp + t0 * a.vs.st, a.vs, row, 8 * c, cols, n, x.vec_v);
-                }
-            } else {
-                // eight channels of two tokens each way: pairs of tokens lie together in V^T
-#pragma unroll 2
-                for (int i = lt; i < 32 * 2 * NW; i += kLoaders) {
-                    const int tp = i % 32, c = i / 32;
-                    const uint4 w0 = octet<false>(vp + t0 * a.vs.st, a.vs, 8 * c, 2 * tp, cols, n, x.vec_v);
-                    const uint4 w1 = octet<false>(vp + t0 * a.vs.st, a.vs, 8 * c, 2 * tp + 1, cols, n, x.vec_v);
-                    const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint32_t*>(&st.v[8 * c + j][2 * tp]) =
-                            __byte_perm(u0[j >> 1], u1[j >> 1], (j & 1) ? 0x7632 : 0x5410);
-                }
-            }
+            load_scaled<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, mk, f->kmul, a.dk, n, x.vec_k, lt);
+            load_scaled<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, mq, f->qmul, a.dk, n, x.vec_q, lt);
+            load_values<NW, FIRST>(st.v, vp + t0 * a.vs.st, a.vs, cols, n, x.vec_v, lt);
             tc::mbar_arrive(&sm.full[s]);
         }
         // the last copies have landed before the CTA may end: the scanning warps wait for every stage
