@@ -62,13 +62,17 @@ struct Params {
     uint32_t* status;
 };
 
+// Epilogue staging (channels_first = 0): a warp's 32 rows x 32 columns of bf16, rows 80 bytes apart (five sixteenths
+// of the banks: eight rows' 16-byte pieces meet none twice).
+constexpr uint32_t kEpiRow = 80, kEpiWarp = 32 * kEpiRow;
+
 template <int BN>
 struct Cfg {
     static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
     static constexpr uint32_t kBTile = BN * BKB;
     static constexpr uint32_t kStageBytes = kATile + kBTile;
     static constexpr uint32_t kTmemCols = 2 * BN;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256 + 2 * BN * 4 + 8 * kEpiWarp;
 };
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -81,6 +85,21 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b
 
 // kind::f8f6f4: fp32 accumulator, A and B e4m3 (format 0), both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }
+
+// acc += v f on pairs (one instruction for two fp32 multiply-adds)
+__device__ __forceinline__ void fma2(uint64_t& acc, float v0, float v1, uint64_t f2) {
+    uint64_t v2;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v2) : "f"(v0), "f"(v1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v2), "l"(f2));
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+    return f;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
 
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -96,8 +115,10 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* mma_done = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    float* s_bias = reinterpret_cast<float*>(stages + kStages * kStageBytes + 256);
+    uint8_t* epi = reinterpret_cast<uint8_t*>(s_bias + 2 * BN);
 
-    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = int(threadIdx.x) & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
@@ -174,86 +195,115 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int q = warp & 3, half = (warp - 4) >> 2, wt = int(threadIdx.x) & 127;
         const uint32_t t_col = tmem + uint32_t(half * CW) + (uint32_t(32 * q) << 16);
+        uint8_t* stage = epi + (warp - 4) * kEpiWarp;
         int64_t kc = 0;
+        int it = 0;
         bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const int64_t m = tile / p.tiles_n * BM + 32 * q + lane, n0 = tile % p.tiles_n * BN + half * CW;
+        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++it) {
+            const int64_t m0 = tile / p.tiles_n * BM + 32 * q, m = m0 + lane, n0 = tile % p.tiles_n * BN + half * CW;
             const bool live = m < p.M;
             const int64_t b = live ? m / p.L : 0, l = live ? m - b * p.L : 0;
             const float* xs = p.xs + b * p.kblocks * p.L + l;
             const float* ws = p.ws + (n0 < p.N ? n0 / 128 : 0) * p.kblocks;
-            float acc[CW];
+            // this half's bias, double buffered: one barrier a tile keeps writers and readers of a buffer apart
+            float* bias = s_bias + (it & 1) * BN + half * CW;
+            if (wt < CW) bias[wt] = (p.bias && n0 + wt < p.N) ? __ldg(p.bias + n0 + wt) : 0.0f;
+            bar_sync(1 + half, 128);
+            uint64_t acc[CW / 2];                 // pairs of neighbouring columns
 #pragma unroll
-            for (int i = 0; i < CW; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
             float f = live ? __ldg(xs) * __ldg(ws) : 0.0f;
+#pragma unroll 1
             for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
                 const int buf = int(kc & 1);
                 float next = 0.0f;                // the next block's factor, loaded under this block
                 if (live && kb + 1 < p.kblocks) next = __ldg(xs + (kb + 1) * p.L) * __ldg(ws + kb + 1);
+                uint64_t f2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
                 if (!tc::mbar_wait(&acc_full[buf], uint32_t(kc >> 1) & 1u, p.budget_ns)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
+                float v[2][16];                   // 16 columns load under the multiply-adds of 16
+                tc::tmem_ld16(t_col + uint32_t(buf * BN), v[0]);
 #pragma unroll
-                for (int c = 0; c < CW; c += 32) {
-                    float v[32];
-                    tc::tmem_ld32(t_col + uint32_t(buf * BN + c), v);
+                for (int c = 0; c < CW / 16; ++c) {
                     tc::tmem_ld_wait();
-                    if (c + 32 == CW) {
+                    if (c + 1 < CW / 16) {
+                        tc::tmem_ld16(t_col + uint32_t(buf * BN + 16 * (c + 1)), v[(c + 1) & 1]);
+                    } else {
                         tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(v[i], f, acc[c + i]);
+                    for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f2);
                 }
                 f = next;
             }
-            if (!ok) {
-#pragma unroll
-                for (int i = 0; i < CW; ++i) acc[i] = __int_as_float(0x7fffffff);
+            if (!ok) {                            // a wait ran out: NaN for this row's outputs
+                for (int i = 0; live && i < CW && n0 + i < p.N; ++i)
+                    p.out[p.channels_first ? (b * p.N + n0 + i) * p.L + l : m * p.N + n0 + i] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+                break;
             }
             if (p.channels_first) {
+                bf16* o = p.out + (b * p.N + n0) * p.L + l;
                 // lanes are neighbouring positions: two columns a step, an even lane takes the pair of the first, an
                 // odd one that of the second, where pairs are aligned and stay in one batch row (L even)
                 if ((p.L & 1) == 0) {
-                    bf16* o = p.out + (b * p.N + n0 + (lane & 1)) * p.L + (l & ~int64_t(1));
+                    o += (lane & 1) ? p.L - 1 : 0;
 #pragma unroll
                     for (int i = 0; i < CW; i += 2) {
-                        const float b0 = (p.bias && n0 + i < p.N) ? __ldg(p.bias + n0 + i) : 0.0f;
-                        const float b1 = (p.bias && n0 + i + 1 < p.N) ? __ldg(p.bias + n0 + i + 1) : 0.0f;
-                        const float x = acc[i] + b0, y = acc[i + 1] + b1;
+                        const float2 a = unpair(acc[i / 2]), bb = *reinterpret_cast<const float2*>(bias + i);
+                        const float x = a.x + bb.x, y = a.y + bb.y;
                         const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
                         const uint32_t w = (lane & 1) ? tc::pack2(other, y) : tc::pack2(x, other);
-                        if (live && n0 + i + (lane & 1) < p.N) *reinterpret_cast<uint32_t*>(o + int64_t(i) * p.L) = w;
+                        if (live && n0 + i + (lane & 1) < p.N) *reinterpret_cast<uint32_t*>(o) = w;
+                        o += 2 * p.L;
                     }
-                } else if (live) {
-                    bf16* o = p.out + (b * p.N + n0) * p.L + l;
+                } else {
 #pragma unroll
-                    for (int i = 0; i < CW; ++i)
-                        if (n0 + i < p.N) o[int64_t(i) * p.L] = __float2bfloat16_rn(acc[i] + (p.bias ? __ldg(p.bias + n0 + i) : 0.0f));
+                    for (int i = 0; i < CW; i += 2) {
+                        const float2 a = unpair(acc[i / 2]), bb = *reinterpret_cast<const float2*>(bias + i);
+                        if (live && n0 + i < p.N) o[0] = __float2bfloat16_rn(a.x + bb.x);
+                        if (live && n0 + i + 1 < p.N) o[p.L] = __float2bfloat16_rn(a.y + bb.y);
+                        o += 2 * p.L;
+                    }
                 }
-            } else if (live) {
-                bf16* o = p.out + m * p.N + n0;
-                const bool wide = (p.N & 7) == 0;
+            } else {
+                // 32 columns of the warp's 32 rows at a time through shared memory: 64 contiguous bytes a row leave
 #pragma unroll
-                for (int i = 0; i < CW; i += 8) {
-                    if (n0 + i >= p.N) break;
-                    if (p.bias) {
+                for (int c = 0; c < CW; c += 32) {
+                    __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[i + j] += n0 + i + j < p.N ? __ldg(p.bias + n0 + i + j) : 0.0f;
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 a = unpair(acc[c / 2 + 4 * j + i]);
+                            const float2 bb = *reinterpret_cast<const float2*>(bias + c + 8 * j + 2 * i);
+                            w[i] = tc::pack2(a.x + bb.x, a.y + bb.y);
+                        }
+                        *reinterpret_cast<uint4*>(stage + lane * kEpiRow + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    if (wide) {
-                        *reinterpret_cast<uint4*>(o + i) =
-                            make_uint4(tc::pack2(acc[i], acc[i + 1]), tc::pack2(acc[i + 2], acc[i + 3]),
-                                       tc::pack2(acc[i + 4], acc[i + 5]), tc::pack2(acc[i + 6], acc[i + 7]));
-                    } else {
+                    __syncwarp();
+                    if ((p.N & 7) == 0) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (n0 + i + j < p.N) o[i + j] = __float2bfloat16_rn(acc[i + j]);
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 8 * j + (lane >> 2), k = lane & 3;
+                            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kEpiRow + 16 * k);
+                            const int64_t n = n0 + c + 8 * k;
+                            if (m0 + r < p.M && n < p.N) *reinterpret_cast<uint4*>(p.out + (m0 + r) * p.N + n) = w;
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int r = 0; r < 32; ++r) {
+                            const bf16 w = *reinterpret_cast<const bf16*>(stage + r * kEpiRow + 2 * lane);
+                            if (m0 + r < p.M && n0 + c + lane < p.N) p.out[(m0 + r) * p.N + n0 + c + lane] = w;
+                        }
                     }
                 }
             }
