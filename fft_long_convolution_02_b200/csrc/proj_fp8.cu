@@ -32,6 +32,7 @@
 
 #include <string>
 
+#include "common.cuh"
 #include "hyena.h"
 #include "kernels.h"
 #include "tc_util.cuh"
@@ -48,11 +49,12 @@ using bf16 = __nv_bfloat16;
 constexpr int BM = 128, BKB = 128;                // rows of a tile, bytes of a block
 constexpr int kThreads = 384;
 constexpr uint32_t kATile = BM * BKB;
+constexpr int kRing = 8, kAhead = 7;               // rows' scales in flight
 
 struct Params {
     int64_t M, L, N, K;
     int kblocks;
-    int64_t tiles_m, tiles_n;
+    int tiles_m, tiles_n;                         // their product below 2^31
     const float* xs;                              // [B][kblocks][L]
     const float* ws;                              // [N / 128][kblocks]
     const float* bias;                            // [N] or nullptr
@@ -72,7 +74,7 @@ struct Cfg {
     static constexpr uint32_t kBTile = BN * BKB;
     static constexpr uint32_t kStageBytes = kATile + kBTile;
     static constexpr uint32_t kTmemCols = 2 * BN;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256 + 2 * BN * 4 + 8 * kEpiWarp;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256 + 2 * BN * 4 + 8 * kEpiWarp + kRing * 256 * 4;
 };
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -117,6 +119,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     float* s_bias = reinterpret_cast<float*>(stages + kStages * kStageBytes + 256);
     uint8_t* epi = reinterpret_cast<uint8_t*>(s_bias + 2 * BN);
+    float* s_ring = reinterpret_cast<float*>(epi + 8 * kEpiWarp);
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = int(threadIdx.x) & 31;
     if (threadIdx.x == 0) {
@@ -135,77 +138,119 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int64_t tiles = p.tiles_m * p.tiles_n;
+    const int tiles = p.tiles_m * p.tiles_n;
 
     // registers: 384 x 168 at launch = 128 x 40 + 256 x 232
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
-        if (warp == 0) {
-            if (lane == 0) {
-                int64_t kc = 0;
-                bool ok = true;
-                for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                    const int m0 = int(tile / p.tiles_n * BM), n0 = int(tile % p.tiles_n * BN);
-                    for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
-                        const int s = int(kc % kStages);
-                        if (!tc::mbar_wait(&empty[s], (uint32_t(kc / kStages) & 1u) ^ 1u, p.budget_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t* sa = stages + s * kStageBytes;
-                        tc::mbar_expect_tx(&full[s], kStageBytes);
-                        tc::tma_load_2d(sa, &map_x, kb * BKB, m0, &full[s]);
-                        tc::tma_load_2d(sa + kATile, &map_w, kb * BKB, n0, &full[s]);
+        // one thread each: stage and buffer counters step, nothing is divided, so that issuing stays under the products
+        if (warp == 0 && lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t phase = 1;                   // of `empty`: the first round finds the stages free
+            bool ok = true;
+            for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x)) {
+                const int m0 = tile / p.tiles_n * BM, n0 = tile % p.tiles_n * BN;
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    if (!tc::mbar_wait(&empty[s], phase, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sa = stages + s * kStageBytes;
+                    tc::mbar_expect_tx(&full[s], kStageBytes);
+                    tc::tma_load_2d(sa, &map_x, kb * BKB, m0, &full[s]);
+                    tc::tma_load_2d(sa + kATile, &map_w, kb * BKB, n0, &full[s]);
+                    issued = min(issued + 1, kStages);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
                     }
                 }
-                if (!ok) report_status(p.status, kStatusTimeout);
-                // nothing left in flight: the last load of every stage has landed
-                for (int64_t j = kc - 1; j >= 0 && j >= kc - kStages; --j)
-                    tc::mbar_wait(&full[j % kStages], uint32_t(j / kStages) & 1u, p.budget_ns);
             }
-        } else if (warp == 1) {
-            if (lane == 0) {
-                constexpr uint32_t idesc = idesc_e4m3(BM, BN);
-                int64_t kc = 0;
-                bool ok = true;
-                for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                    for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
-                        const int s = int(kc % kStages), acc = int(kc & 1);
-                        if (!tc::mbar_wait(&acc_empty[acc], (uint32_t(kc >> 1) & 1u) ^ 1u, p.budget_ns) ||
-                            !tc::mbar_wait(&full[s], uint32_t(kc / kStages) & 1u, p.budget_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after_sync();
-                        const uint32_t sa = tc::smem_u32(stages + s * kStageBytes), sb = sa + kATile;
-                        // the tail of the last block lies behind K: zeros, and no products for whole steps of them
-                        const int steps = min(4, int((p.K - int64_t(kb) * BKB + 31) / 32));
-                        for (int ks = 0; ks < steps; ++ks)
-                            mma_e4m3(tmem + uint32_t(acc) * BN, tc::desc_sw128(sa + uint32_t(ks) * 32u, 16, 1024),
-                                     tc::desc_sw128(sb + uint32_t(ks) * 32u, 16, 1024), idesc, ks > 0);
-                        tc::commit(&empty[s]);
-                        tc::commit(&acc_full[acc]);
-                    }
+            if (!ok) report_status(p.status, kStatusTimeout);
+            // nothing left in flight: the last load of every stage has landed
+            for (; issued > 0; --issued) {
+                if (s == 0) {
+                    s = kStages;
+                    phase ^= 1u;
                 }
-                if (!ok) report_status(p.status, kStatusTimeout);
-                // nothing left in flight before tensor memory is released
-                tc::commit(mma_done);
-                if (!tc::mbar_wait(mma_done, 0, p.budget_ns)) report_status(p.status, kStatusTimeout);
+                --s;
+                tc::mbar_wait(&full[s], phase ^ 1u, p.budget_ns);
             }
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+            const uint64_t da0 = tc::desc_sw128(tc::smem_u32(stages), 16, 1024), db0 = da0 + (kATile >> 4);
+            const int tail = int((p.K - int64_t(p.kblocks - 1) * BKB + 31) / 32);     // products of the last block
+            int s = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x)) {
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    if (!tc::mbar_wait(&acc_empty[acc], acc_phase, p.budget_ns) ||
+                        !tc::mbar_wait(&full[s], phase, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t da = da0 + uint32_t(s) * (kStageBytes >> 4), db = db0 + uint32_t(s) * (kStageBytes >> 4);
+                    const uint32_t d = tmem + uint32_t(acc) * BN;
+                    // the tail of the last block lies behind K: zeros, and no products for whole steps of them
+                    const int steps = kb + 1 < p.kblocks ? 4 : tail;
+                    mma_e4m3(d, da, db, idesc, 0u);
+                    if (steps > 1) mma_e4m3(d, da + 2, db + 2, idesc, 1u);
+                    if (steps > 2) mma_e4m3(d, da + 4, db + 4, idesc, 1u);
+                    if (steps > 3) mma_e4m3(d, da + 6, db + 6, idesc, 1u);
+                    tc::commit(&acc_full[acc]);
+                    tc::commit(&empty[s]);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                    acc ^= 1;
+                    acc_phase ^= acc == 0;
+                }
+            }
+            if (!ok) report_status(p.status, kStatusTimeout);
+            // nothing left in flight before tensor memory is released
+            tc::commit(mma_done);
+            if (!tc::mbar_wait(mma_done, 0, p.budget_ns)) report_status(p.status, kStatusTimeout);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
         const int q = warp & 3, half = (warp - 4) >> 2, wt = int(threadIdx.x) & 127;
         const uint32_t t_col = tmem + uint32_t(half * CW) + (uint32_t(32 * q) << 16);
         uint8_t* stage = epi + (warp - 4) * kEpiWarp;
-        int64_t kc = 0;
-        int it = 0;
+        // The rows' scales come kAhead blocks ahead (a block's products take less than a load under traffic), across
+        // tiles, by asynchronous 4-byte copies into a ring of this thread's own slots.
+        float* ring = s_ring + (int(threadIdx.x) - 128);
+        int pt = int(blockIdx.x), pc = 0;         // the tile and the ring's slot to fetch next
+        int pkb = p.kblocks;
+        const float* px = nullptr;
+        bool plive = false;
+        auto fetch = [&]() {
+            if (pkb == p.kblocks) {               // enter tile pt
+                const uint32_t m = uint32_t(pt / p.tiles_n) * BM + 32 * q + lane;
+                plive = pt < tiles && m < p.M;
+                const int64_t b = plive ? m / uint32_t(p.L) : 0;
+                px = p.xs + b * (p.kblocks - 1) * p.L + (plive ? m : 0);
+                pt += int(gridDim.x);
+                pkb = 0;
+            }
+            if (plive) cp_async_small<4>(ring + pc * 256, px);
+            cp_async_commit();
+            px += p.L;
+            ++pkb;
+            pc = (pc + 1) % kRing;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kAhead; ++i) fetch();
+        int buf = 0, slot = 0, it = 0;
+        uint32_t phase = 0;
         bool ok = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++it) {
-            const int64_t m0 = tile / p.tiles_n * BM + 32 * q, m = m0 + lane, n0 = tile % p.tiles_n * BN + half * CW;
+        for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x), ++it) {
+            const int tm = tile / p.tiles_n;
+            const int64_t m0 = int64_t(tm) * BM + 32 * q, m = m0 + lane, n0 = int64_t(tile - tm * p.tiles_n) * BN + half * CW;
             const bool live = m < p.M;
-            const int64_t b = live ? m / p.L : 0, l = live ? m - b * p.L : 0;
-            const float* xs = p.xs + b * p.kblocks * p.L + l;
+            const int64_t b = live ? uint32_t(m) / uint32_t(p.L) : 0, l = live ? m - b * p.L : 0;
             const float* ws = p.ws + (n0 < p.N ? n0 / 128 : 0) * p.kblocks;
             // this half's bias, double buffered: one barrier a tile keeps writers and readers of a buffer apart
             float* bias = s_bias + (it & 1) * BN + half * CW;
@@ -214,15 +259,15 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             uint64_t acc[CW / 2];                 // pairs of neighbouring columns
 #pragma unroll
             for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
-            float f = live ? __ldg(xs) * __ldg(ws) : 0.0f;
 #pragma unroll 1
-            for (int kb = 0; kb < p.kblocks; ++kb, ++kc) {
-                const int buf = int(kc & 1);
-                float next = 0.0f;                // the next block's factor, loaded under this block
-                if (live && kb + 1 < p.kblocks) next = __ldg(xs + (kb + 1) * p.L) * __ldg(ws + kb + 1);
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
+                const float f = live ? ring[slot * 256] * __ldg(ws + kb) : 0.0f;
+                slot = (slot + 1) % kRing;
+                fetch();
                 uint64_t f2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
-                if (!tc::mbar_wait(&acc_full[buf], uint32_t(kc >> 1) & 1u, p.budget_ns)) {
+                if (!tc::mbar_wait(&acc_full[buf], phase, p.budget_ns)) {
                     ok = false;
                     break;
                 }
@@ -242,7 +287,8 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f2);
                 }
-                f = next;
+                buf ^= 1;
+                phase ^= buf == 0;
             }
             if (!ok) {                            // a wait ran out: NaN for this row's outputs
                 for (int i = 0; live && i < CW && n0 + i < p.N; ++i)
@@ -374,7 +420,7 @@ k_proj_fp8_few(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ wq, P
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int m = 8 * i + 2 * t + j;
-                const float f = m < M ? sw * __ldg(p.xs + (int64_t(m) / p.L * p.kblocks + kb) * p.L + int64_t(m) % p.L) : 0.0f;
+                const float f = m < M ? sw * __ldg(p.xs + (int64_t(uint32_t(m) / uint32_t(p.L)) * p.kblocks + kb) * p.L + uint32_t(m) % uint32_t(p.L)) : 0.0f;
                 acc[i][j] = fmaf(c[j], f, acc[i][j]);
                 acc[i][j + 2] = fmaf(c[j + 2], f, acc[i][j + 2]);
             }
@@ -397,7 +443,7 @@ k_proj_fp8_few(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ wq, P
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) s += red[w][r][m];
         if (p.bias) s += __ldg(p.bias + n);
-        const int64_t b = m / p.L, l = m - b * p.L;
+        const int64_t b = uint32_t(m) / uint32_t(p.L), l = m - b * p.L;
         p.out[p.channels_first ? (b * p.N + n) * p.L + l : int64_t(m) * p.N + n] = __float2bfloat16_rn(s);
     }
 }
@@ -433,9 +479,9 @@ template <int BN>
 cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, Params& p, int sms, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_proj_fp8<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<BN>::kSmem));
     if (e != cudaSuccess) return e;
-    p.tiles_m = (p.M + BM - 1) / BM;
-    p.tiles_n = (p.N + BN - 1) / BN;
-    const int64_t tiles = p.tiles_m * p.tiles_n;
+    p.tiles_m = int((p.M + BM - 1) / BM);
+    p.tiles_n = int((p.N + BN - 1) / BN);
+    const int tiles = p.tiles_m * p.tiles_n;
     k_proj_fp8<BN><<<unsigned(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s>>>(mx, mw, p);
     return cudaGetLastError();
 }
@@ -457,9 +503,10 @@ extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const 
     if (!xq || !xs || !Wq || !Ws || !out) return fail(HYENA_ERR_INVALID_ARG, "xq, xs, Wq, Ws and out must not be NULL");
     if (B < 1 || L < 1 || K < 1 || N < 1) return fail(HYENA_ERR_INVALID_ARG, "B, L, K and N must be >= 1");
     if (K % 16 != 0 || K > (int64_t(1) << 20) || N > (int64_t(1) << 20) || B > 65535 || L > (int64_t(1) << 31) - 1 ||
-        B * L > (int64_t(1) << 31) - 1)
+        B * L > (int64_t(1) << 31) - 1 || (B * L + BM - 1) / BM * ((N + 63) / 64) > (int64_t(1) << 31) - 1)
         return fail(HYENA_ERR_UNSUPPORTED_SHAPE,
-                    "K must be a multiple of 16, K and N at most 2^20, B <= 65535 and B * L < 2^31");
+                    "K must be a multiple of 16, K and N at most 2^20, B <= 65535, B * L < 2^31 and the output of fewer "
+                    "than 2^31 tiles");
     if (!aligned(xq, 16) || !aligned(Wq, 16) || !aligned(out, 16))
         return fail(HYENA_ERR_MISALIGNED, "xq, Wq and out must be 16-byte aligned");
     if (!aligned(xs, 4) || !aligned(Ws, 4) || !aligned(bias, 4))
