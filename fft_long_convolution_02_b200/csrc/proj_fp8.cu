@@ -7,19 +7,25 @@
 // The scales are arbitrary fp32 numbers, so the tensor cores form one block's
 // P in fp32 and the CUDA cores add it, scaled, to fp32 sums in registers.
 //
-// k_proj_fp8 (more than kFewTokens rows): persistent, one CTA per SM, tiles of
-// 128 rows x BN outputs, 384 threads in three roles:
-//   warp 0     TMA: x and W blocks (128 x 128 and BN x 128 bytes, 128-byte
-//              swizzle) into a ring of stages;
-//   warp 1     tcgen05.mma kind::f8f6f4 (M 128, N BN, K 32; four a block) into
-//              one of two tensor-memory buffers, a commit per block;
-//   warps 4-11 two warpgroups, half of the columns each (their sums take most of
-//              the registers, which the first warpgroup hands over): read a
-//              block's P with tcgen05.ld, free the buffer, add it times the row's factor.  A
-//              thread holds one row, so the factor is one number a block.
-// At BN = 256 a block is 512 cycles of tensor work and 256 of multiply-adds a
-// scheduler, which overlap; the ring and the two buffers let the next tile's
-// products run under this tile's epilogue.
+// k_proj_fp8 (more than kFewTokens rows): persistent, 384 threads a CTA in
+// three roles:
+//   warp 0      TMA: x and W blocks of 128 bytes a row (128-byte swizzle) into a
+//               ring of stages;
+//   warp 1      tcgen05.mma kind::f8f6f4 (K 32; four a block) into one of two
+//               tensor-memory buffers, a commit per block;
+//   warps 4-11  two warpgroups, half of the columns each (their sums take most
+//               of the registers, which the first warpgroup hands over): read a
+//               block's P with tcgen05.ld, free the buffer, add it times the
+//               row's factor.  A thread holds one row, so the factor is one
+//               number a block.
+// Tiles.  Large products run on pairs of CTAs (cta_group::2): 256 x 256, each
+// CTA the sums of its 128 rows and half of the W rows in its shared memory, so
+// a block brings 32 KB into an SM for its 512 cycles of tensor work; a CTA by
+// itself would need 48 KB for 128 x 256, more than L2 gives an SM in that time
+// (measured 0.50 us a block against 0.35 us without the loads).  Smaller ones
+// run on single CTAs with 128 x 128 or 128 x 64 tiles, which reach more SMs.
+// The sums leave through shared memory as TMA stores that run under the next
+// tile's first blocks.
 //
 // k_proj_fp8_few (up to kFewTokens rows): the weights' bytes bound it.  A CTA
 // takes 16 outputs; its 8 warps take the blocks of K in turn, W as the 16-row
@@ -46,10 +52,13 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int BM = 128, BKB = 128;                // rows of a tile, bytes of a block
+constexpr int BM = 128, BKB = 128;                // rows of a CTA's tile, bytes of a block
 constexpr int kThreads = 384;
 constexpr uint32_t kATile = BM * BKB;
-constexpr int kRing = 8, kAhead = 7;               // rows' scales in flight
+constexpr int kRing = 8, kAhead = 7;              // scales in flight
+
+// How a tile leaves: element by element, or as TMA stores of the tensor map `map_o`.
+enum Store { STORE_PLAIN = 0, STORE_TMA = 1 };
 
 struct Params {
     int64_t M, L, N, K;
@@ -59,34 +68,90 @@ struct Params {
     const float* ws;                              // [N / 128][kblocks]
     const float* bias;                            // [N] or nullptr
     bf16* out;
-    int channels_first;
+    int channels_first, store;
     uint64_t budget_ns;
     uint32_t* status;
 };
 
-// Epilogue staging (channels_first = 0): a warp's 32 rows x 32 columns of bf16, rows 80 bytes apart (five sixteenths
-// of the banks: eight rows' 16-byte pieces meet none twice).
-constexpr uint32_t kEpiRow = 80, kEpiWarp = 32 * kEpiRow;
-
-template <int BN>
+// BN columns a tile; G CTAs share one (G = 2: 256 rows).
+template <int BN, int G>
 struct Cfg {
-    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-    static constexpr uint32_t kBTile = BN * BKB;
+    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 4 : 6);
+    static constexpr uint32_t kBTile = BN / G * BKB;
     static constexpr uint32_t kStageBytes = kATile + kBTile;
     static constexpr uint32_t kTmemCols = 2 * BN;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256 + 2 * BN * 4 + 8 * kEpiWarp + kRing * 256 * 4;
+    static constexpr int CW = BN / 2;             // columns a consuming thread
+    // Pairs hand over each half of the columns by itself: a buffer's round trip (products, reading, arrivals across the
+    // pair) is longer than two blocks' products, and half as much is read in half of them.
+    static constexpr int H = G;
+    static constexpr uint32_t kOutWarp = 32 * CW * 2;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 8 * kOutWarp + 512 + 8 * CW * 4 + 2 * kRing * 256 * 4;
 };
 
+template <int G>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    if constexpr (G == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
 // kind::f8f6f4: fp32 accumulator, A and B e4m3 (format 0), both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }
+
+// An arrival at this barrier of every CTA that shares the tile, once the products issued so far are done.
+template <int G>
+__device__ __forceinline__ void commit(uint64_t* mbar) {
+    if constexpr (G == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                tc::smem_u32(mbar)),
+            "h"(uint16_t(3))
+            : "memory");
+    else
+        tc::commit(mbar);
+}
+
+// A load into this CTA's memory whose bytes count at the first CTA's barrier (the peer bit of the address cleared).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(tc::smem_u32(mbar) & 0xFEFFFFFFu)
+        : "memory");
+}
+
+// An arrival at CTA 0's barrier.
+__device__ __forceinline__ void arrive_first(uint64_t* mbar) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(remote) : "r"(tc::smem_u32(mbar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(remote) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+
+template <int G>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    if constexpr (G == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(tc::smem_u32(slot)), "r"(cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    } else {
+        tc::tmem_alloc(slot, cols);
+    }
+}
+template <int G>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
+    if constexpr (G == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(base), "r"(cols));
+    else tc::tmem_dealloc(base, cols);
+}
 
 // acc += v f on pairs (one instruction for two fp32 multiply-adds)
 __device__ __forceinline__ void fma2(uint64_t& acc, float v0, float v1, uint64_t f2) {
@@ -99,43 +164,51 @@ __device__ __forceinline__ float2 unpair(uint64_t x) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
     return f;
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
-}
-
-template <int BN>
+template <int BN, int G>
 __global__ void __launch_bounds__(kThreads, 1)
-k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, Params p) {
-    constexpr int kStages = Cfg<BN>::kStages;
-    constexpr uint32_t kStageBytes = Cfg<BN>::kStageBytes;
-    constexpr int CW = BN / 2;                    // columns a thread
+k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+           const __grid_constant__ CUtensorMap map_o, Params p) {
+    using Cf = Cfg<BN, G>;
+    constexpr int kStages = Cf::kStages;
+    constexpr uint32_t kStageBytes = Cf::kStageBytes;
+    constexpr int CW = Cf::CW, H = Cf::H;
     extern __shared__ __align__(1024) uint8_t smem_p[];
+    // the same offset in both CTAs of a pair: the base is the kernel's own in each
     uint8_t* stages = smem_p + ((1024u - (tc::smem_u32(smem_p) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(stages + kStages * kStageBytes);
+    uint8_t* out_stage = stages + kStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + 8 * Cf::kOutWarp);
     uint64_t* empty = full + kStages;
-    uint64_t* acc_full = empty + kStages;
-    uint64_t* acc_empty = acc_full + 2;
-    uint64_t* mma_done = acc_empty + 2;
+    uint64_t* acc_full = empty + kStages;         // [half][buffer]
+    uint64_t* acc_empty = acc_full + 4;
+    uint64_t* out_full = acc_empty + 4;           // [half]: its four warps have staged their part
+    uint64_t* out_free = out_full + 2;            // [half]: the staging has been read
+    uint64_t* mma_done = out_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-    float* s_bias = reinterpret_cast<float*>(stages + kStages * kStageBytes + 256);
-    uint8_t* epi = reinterpret_cast<uint8_t*>(s_bias + 2 * BN);
-    float* s_ring = reinterpret_cast<float*>(epi + 8 * kEpiWarp);
+    float* s_bias = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 512);
+    float* s_ring = s_bias + 8 * CW;
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = int(threadIdx.x) & 31;
+    const int rank = G == 2 ? int(blockIdx.x) & 1 : 0;             // in the pair; the first issues the products
+    const int first = int(blockIdx.x) / G, step = int(gridDim.x) / G;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < 4; ++a) {
             tc::mbar_init(&acc_full[a], 1);
-            tc::mbar_init(&acc_empty[a], 8);      // one arrival a reading warp
+            tc::mbar_init(&acc_empty[a], 8 / H * G);               // one arrival a reading warp
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(&out_full[a], 4);
+            tc::mbar_init(&out_free[a], 1);
         }
         tc::mbar_init(mma_done, 1);
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, Cfg<BN>::kTmemCols);
+    if (warp == 1) tmem_alloc<G>(tmem_slot, Cf::kTmemCols);
     tc::fence_before_sync();
-    __syncthreads();
+    if constexpr (G == 2) cluster_sync();
+    else __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int tiles = p.tiles_m * p.tiles_n;
@@ -148,17 +221,28 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             int s = 0, issued = 0;
             uint32_t phase = 1;                   // of `empty`: the first round finds the stages free
             bool ok = true;
-            for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x)) {
-                const int m0 = tile / p.tiles_n * BM, n0 = tile % p.tiles_n * BN;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                const int tm = tile / p.tiles_n;
+                const int m0 = (tm * G + rank) * BM, n0 = (tile - tm * p.tiles_n) * BN;
                 for (int kb = 0; kb < p.kblocks; ++kb) {
                     if (!tc::mbar_wait(&empty[s], phase, p.budget_ns)) {
                         ok = false;
                         break;
                     }
                     uint8_t* sa = stages + s * kStageBytes;
-                    tc::mbar_expect_tx(&full[s], kStageBytes);
-                    tc::tma_load_2d(sa, &map_x, kb * BKB, m0, &full[s]);
-                    tc::tma_load_2d(sa + kATile, &map_w, kb * BKB, n0, &full[s]);
+                    if constexpr (G == 2) {
+                        // the first CTA's barrier counts the bytes of both
+                        if (rank == 0) tc::mbar_expect_tx(&full[s], 2 * kStageBytes);
+                        tma_load_pair(sa, &map_x, kb * BKB, m0, &full[s]);
+                        // each CTA holds half of the W rows of each half of the columns
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_pair(sa + kATile + h * (BN / 4) * BKB, &map_w, kb * BKB, n0 + h * CW + rank * (BN / 4), &full[s]);
+                    } else {
+                        tc::mbar_expect_tx(&full[s], kStageBytes);
+                        tc::tma_load_2d(sa, &map_x, kb * BKB, m0, &full[s]);
+                        tc::tma_load_2d(sa + kATile, &map_w, kb * BKB, n0, &full[s]);
+                    }
                     issued = min(issued + 1, kStages);
                     if (++s == kStages) {
                         s = 0;
@@ -167,40 +251,46 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 }
             }
             if (!ok) report_status(p.status, kStatusTimeout);
-            // nothing left in flight: the last load of every stage has landed
+            // nothing left in flight: the last loads have landed when their products are done, or (one CTA) at `full`
             for (; issued > 0; --issued) {
                 if (s == 0) {
                     s = kStages;
                     phase ^= 1u;
                 }
                 --s;
-                tc::mbar_wait(&full[s], phase ^ 1u, p.budget_ns);
+                if constexpr (G == 2) tc::mbar_wait(&empty[s], phase ^ 1u, p.budget_ns);
+                else tc::mbar_wait(&full[s], phase ^ 1u, p.budget_ns);
             }
-        } else if (warp == 1 && lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+            // the second CTA of a pair stays until the last arrival at its barriers
+            if (rank == 1) tc::mbar_wait(mma_done, 0, p.budget_ns);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(BM * G, BN / H);
             const uint64_t da0 = tc::desc_sw128(tc::smem_u32(stages), 16, 1024), db0 = da0 + (kATile >> 4);
             const int tail = int((p.K - int64_t(p.kblocks - 1) * BKB + 31) / 32);     // products of the last block
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 1;
             bool ok = true;
-            for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x)) {
-                for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (!tc::mbar_wait(&acc_empty[acc], acc_phase, p.budget_ns) ||
-                        !tc::mbar_wait(&full[s], phase, p.budget_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint64_t da = da0 + uint32_t(s) * (kStageBytes >> 4), db = db0 + uint32_t(s) * (kStageBytes >> 4);
-                    const uint32_t d = tmem + uint32_t(acc) * BN;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                for (int kb = 0; kb < p.kblocks && ok; ++kb) {
+                    ok = tc::mbar_wait(&full[s], phase, p.budget_ns);
+                    const uint64_t da = da0 + uint32_t(s) * (kStageBytes >> 4);
                     // the tail of the last block lies behind K: zeros, and no products for whole steps of them
                     const int steps = kb + 1 < p.kblocks ? 4 : tail;
-                    mma_e4m3(d, da, db, idesc, 0u);
-                    if (steps > 1) mma_e4m3(d, da + 2, db + 2, idesc, 1u);
-                    if (steps > 2) mma_e4m3(d, da + 4, db + 4, idesc, 1u);
-                    if (steps > 3) mma_e4m3(d, da + 6, db + 6, idesc, 1u);
-                    tc::commit(&acc_full[acc]);
-                    tc::commit(&empty[s]);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        ok = ok && tc::mbar_wait(&acc_empty[2 * h + acc], acc_phase, p.budget_ns);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const uint64_t db = db0 + uint32_t(s) * (kStageBytes >> 4) + h * ((BN / 4 * BKB) >> 4);
+                        const uint32_t d = tmem + uint32_t(acc) * BN + h * CW;
+                        mma_e4m3<G>(d, da, db, idesc, 0u);
+                        if (steps > 1) mma_e4m3<G>(d, da + 2, db + 2, idesc, 1u);
+                        if (steps > 2) mma_e4m3<G>(d, da + 4, db + 4, idesc, 1u);
+                        if (steps > 3) mma_e4m3<G>(d, da + 6, db + 6, idesc, 1u);
+                        commit<G>(&acc_full[2 * h + acc]);
+                    }
+                    if (!ok) break;
+                    commit<G>(&empty[s]);
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1u;
@@ -211,69 +301,80 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             }
             if (!ok) report_status(p.status, kStatusTimeout);
             // nothing left in flight before tensor memory is released
-            tc::commit(mma_done);
+            commit<G>(mma_done);
             if (!tc::mbar_wait(mma_done, 0, p.budget_ns)) report_status(p.status, kStatusTimeout);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
-        const int q = warp & 3, half = (warp - 4) >> 2, wt = int(threadIdx.x) & 127;
+        const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t t_col = tmem + uint32_t(half * CW) + (uint32_t(32 * q) << 16);
-        uint8_t* stage = epi + (warp - 4) * kEpiWarp;
-        // The rows' scales come kAhead blocks ahead (a block's products take less than a load under traffic), across
-        // tiles, by asynchronous 4-byte copies into a ring of this thread's own slots.
-        float* ring = s_ring + (int(threadIdx.x) - 128);
-        int pt = int(blockIdx.x), pc = 0;         // the tile and the ring's slot to fetch next
-        int pkb = p.kblocks;
-        const float* px = nullptr;
+        uint8_t* stage = out_stage + (warp - 4) * Cf::kOutWarp;     // (channels_first: a half's four parts together)
+        uint64_t *my_full = acc_full + (H == 2 ? 2 * half : 0), *my_empty = acc_empty + (H == 2 ? 2 * half : 0);
+        float* bias = s_bias + (warp - 4) * CW;
+        // The scales come kAhead blocks ahead (a block's products take less than a load under traffic), across tiles, by
+        // asynchronous 4-byte copies into a ring of this thread's own slots.
+        float2* ring = reinterpret_cast<float2*>(s_ring) + (int(threadIdx.x) - 128);
+        int pt = first, pc = 0, pkb = p.kblocks;  // the tile, the ring's slot and the block to fetch next
+        const float *px = nullptr, *pw = nullptr;
         bool plive = false;
         auto fetch = [&]() {
             if (pkb == p.kblocks) {               // enter tile pt
-                const uint32_t m = uint32_t(pt / p.tiles_n) * BM + 32 * q + lane;
-                plive = pt < tiles && m < p.M;
+                const int tm = pt / p.tiles_n;
+                const uint32_t m = (uint32_t(tm) * G + rank) * BM + 32 * q + lane;
+                const int64_t n = int64_t(pt - tm * p.tiles_n) * BN + half * CW;
+                plive = pt < tiles && m < p.M && n < p.N;
                 const int64_t b = plive ? m / uint32_t(p.L) : 0;
                 px = p.xs + b * (p.kblocks - 1) * p.L + (plive ? m : 0);
-                pt += int(gridDim.x);
+                pw = p.ws + (plive ? n / 128 : 0) * p.kblocks;
+                pt += step;
                 pkb = 0;
             }
-            if (plive) cp_async_small<4>(ring + pc * 256, px);
+            if (plive) {
+                cp_async_small<4>(&ring[pc].x, px);
+                cp_async_small<4>(&ring[pc].y, pw);
+            }
             cp_async_commit();
             px += p.L;
+            ++pw;
             ++pkb;
-            pc = (pc + 1) % kRing;
+            pc = (pc + 256) & (kRing * 256 - 1);
         };
 #pragma unroll 1
         for (int i = 0; i < kAhead; ++i) fetch();
-        int buf = 0, slot = 0, it = 0;
-        uint32_t phase = 0;
+        int buf = 0, slot = 0;
+        uint32_t phase = 0, out_phase = 0;
         bool ok = true;
-        for (int tile = int(blockIdx.x); tile < tiles && ok; tile += int(gridDim.x), ++it) {
+        for (int tile = first; tile < tiles && ok; tile += step) {
             const int tm = tile / p.tiles_n;
-            const int64_t m0 = int64_t(tm) * BM + 32 * q, m = m0 + lane, n0 = int64_t(tile - tm * p.tiles_n) * BN + half * CW;
-            const bool live = m < p.M;
+            const int64_t m0 = (int64_t(tm) * G + rank) * BM + 32 * q, m = m0 + lane;
+            const int64_t n0 = int64_t(tile - tm * p.tiles_n) * BN + half * CW;
+            const bool live = m < p.M, row_in = live && n0 < p.N;
             const int64_t b = live ? uint32_t(m) / uint32_t(p.L) : 0, l = live ? m - b * p.L : 0;
-            const float* ws = p.ws + (n0 < p.N ? n0 / 128 : 0) * p.kblocks;
-            // this half's bias, double buffered: one barrier a tile keeps writers and readers of a buffer apart
-            float* bias = s_bias + (it & 1) * BN + half * CW;
-            if (wt < CW) bias[wt] = (p.bias && n0 + wt < p.N) ? __ldg(p.bias + n0 + wt) : 0.0f;
-            bar_sync(1 + half, 128);
+            // the bias of this warp's columns, its own copy: no barrier that a warp which gave up would leave others at
+            __syncwarp();
+#pragma unroll
+            for (int i = lane; i < CW; i += 32) bias[i] = (p.bias && n0 + i < p.N) ? __ldg(p.bias + n0 + i) : 0.0f;
+            __syncwarp();
             uint64_t acc[CW / 2];                 // pairs of neighbouring columns
 #pragma unroll
             for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < p.kblocks; ++kb) {
-                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
-                const float f = live ? ring[slot * 256] * __ldg(ws + kb) : 0.0f;
-                slot = (slot + 1) % kRing;
-                fetch();
-                uint64_t f2;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
-                if (!tc::mbar_wait(&acc_full[buf], phase, p.budget_ns)) {
+                if (!tc::mbar_wait(&my_full[buf], phase, p.budget_ns)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                float v[2][16];                   // 16 columns load under the multiply-adds of 16
+                // 16 columns load under the multiply-adds of 16, the first while the factor comes
+                float v[2][16];
                 tc::tmem_ld16(t_col + uint32_t(buf * BN), v[0]);
+                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
+                const float2 sc = ring[slot];
+                const float f = row_in ? sc.x * sc.y : 0.0f;
+                uint64_t f2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+                slot = (slot + 256) & (kRing * 256 - 1);
+                fetch();
 #pragma unroll
                 for (int c = 0; c < CW / 16; ++c) {
                     tc::tmem_ld_wait();
@@ -282,7 +383,10 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     } else {
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
+                        if (lane == 0) {
+                            if constexpr (G == 2) arrive_first(&my_empty[buf]);
+                            else tc::mbar_arrive(&my_empty[buf]);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f2);
@@ -295,22 +399,36 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     p.out[p.channels_first ? (b * p.N + n0 + i) * p.L + l : m * p.N + n0 + i] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
                 break;
             }
+            if (p.store == STORE_TMA) {
+                // the last tile's stores have read the staging
+                if (!p.channels_first || q == 0) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+                    __syncwarp();
+                    if (p.channels_first && lane == 0) tc::mbar_arrive(&out_free[half]);
+                }
+                if (p.channels_first && !tc::mbar_wait(&out_free[half], out_phase, p.budget_ns)) {
+                    ok = false;
+                    break;
+                }
+            }
             if (p.channels_first) {
-                bf16* o = p.out + (b * p.N + n0) * p.L + l;
-                // lanes are neighbouring positions: two columns a step, an even lane takes the pair of the first, an
-                // odd one that of the second, where pairs are aligned and stay in one batch row (L even)
-                if ((p.L & 1) == 0) {
-                    o += (lane & 1) ? p.L - 1 : 0;
+                if (p.store == STORE_TMA) {
+                    // [64 positions' box][column][64 positions], 128-byte swizzle.  Lanes are neighbouring positions: of two
+                    // columns four apart an even lane takes the pair of the first, an odd one that of the second (four
+                    // apart, their pieces lie on different halves of the banks).
+                    uint8_t* so = out_stage + half * (4 * Cf::kOutWarp) + (q >> 1) * (CW * 128) + (lane & 1) * (4 * 128) + ((lane >> 1) & 3) * 4;
+                    const int piece = 4 * (q & 1) + (lane >> 3), odd = (lane & 1) * 4;
 #pragma unroll
-                    for (int i = 0; i < CW; i += 2) {
-                        const float2 a = unpair(acc[i / 2]), bb = *reinterpret_cast<const float2*>(bias + i);
-                        const float x = a.x + bb.x, y = a.y + bb.y;
+                    for (int i = 0; i < CW; ++i) {
+                        if (i & 4) continue;
+                        const float2 a = unpair(acc[i / 2]), e = unpair(acc[(i + 4) / 2]);
+                        const float x = ((i & 1) ? a.y : a.x) + bias[i], y = ((i & 1) ? e.y : e.x) + bias[i + 4];
                         const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
-                        const uint32_t w = (lane & 1) ? tc::pack2(other, y) : tc::pack2(x, other);
-                        if (live && n0 + i + (lane & 1) < p.N) *reinterpret_cast<uint32_t*>(o) = w;
-                        o += 2 * p.L;
+                        *reinterpret_cast<uint32_t*>(so + i * 128 + 16 * (piece ^ ((i + odd) & 7))) =
+                            (lane & 1) ? tc::pack2(other, y) : tc::pack2(x, other);
                     }
                 } else {
+                    bf16* o = p.out + (b * p.N + n0) * p.L + l;
 #pragma unroll
                     for (int i = 0; i < CW; i += 2) {
                         const float2 a = unpair(acc[i / 2]), bb = *reinterpret_cast<const float2*>(bias + i);
@@ -320,45 +438,75 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     }
                 }
             } else {
-                // 32 columns of the warp's 32 rows at a time through shared memory: 64 contiguous bytes a row leave
+                // row `lane` of the warp's 32: in boxes of 64 columns, 128-byte swizzle (of 32, 64-byte swizzle)
+                constexpr int kBox = CW < 64 ? CW : 64;
 #pragma unroll
-                for (int c = 0; c < CW; c += 32) {
-                    __syncwarp();
+                for (int j = 0; j < CW / 8; ++j) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 a = unpair(acc[c / 2 + 4 * j + i]);
-                            const float2 bb = *reinterpret_cast<const float2*>(bias + c + 8 * j + 2 * i);
-                            w[i] = tc::pack2(a.x + bb.x, a.y + bb.y);
-                        }
-                        *reinterpret_cast<uint4*>(stage + lane * kEpiRow + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = unpair(acc[4 * j + i]);
+                        const float2 bb = *reinterpret_cast<const float2*>(bias + 8 * j + 2 * i);
+                        w[i] = tc::pack2(a.x + bb.x, a.y + bb.y);
                     }
+                    const int box = j / (kBox / 8), c = j % (kBox / 8);
+                    const int at = kBox == 64 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
+                    *reinterpret_cast<uint4*>(stage + box * (32 * kBox * 2) + lane * (kBox * 2) + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (p.store == STORE_PLAIN) {
                     __syncwarp();
-                    if ((p.N & 7) == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = 8 * j + (lane >> 2), k = lane & 3;
-                            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kEpiRow + 16 * k);
-                            const int64_t n = n0 + c + 8 * k;
-                            if (m0 + r < p.M && n < p.N) *reinterpret_cast<uint4*>(p.out + (m0 + r) * p.N + n) = w;
-                        }
-                    } else {
 #pragma unroll 4
-                        for (int r = 0; r < 32; ++r) {
-                            const bf16 w = *reinterpret_cast<const bf16*>(stage + r * kEpiRow + 2 * lane);
-                            if (m0 + r < p.M && n0 + c + lane < p.N) p.out[(m0 + r) * p.N + n0 + c + lane] = w;
-                        }
+                    for (int i = lane; i < 32 * CW; i += 32) {
+                        const int r = i / CW, n = i % CW, box = n / kBox, c = (n % kBox) / 8;
+                        const int at = kBox == 64 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                        const bf16 w = *reinterpret_cast<const bf16*>(stage + box * (32 * kBox * 2) + r * (kBox * 2) + 16 * at + 2 * (n & 7));
+                        if (m0 + r < p.M && n0 + n < p.N) p.out[(m0 + r) * p.N + n0 + n] = w;
                     }
+                    __syncwarp();
+                }
+            }
+            if (p.store == STORE_TMA) {
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (p.channels_first) {
+                    if (lane == 0) tc::mbar_arrive(&out_full[half]);
+                    if (q == 0 && !tc::mbar_wait(&out_full[half], out_phase, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    out_phase ^= 1u;
+                }
+                if (lane == 0 && m0 < p.M && n0 < p.N && (!p.channels_first || q == 0)) {
+                    if (p.channels_first) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(&map_o),
+                                         "r"(int(l) + 64 * c), "r"(int(n0)), "r"(int(b)),
+                                         "r"(tc::smem_u32(stage + c * (CW * 128)))
+                                         : "memory");
+                    } else {
+                        constexpr int kBox = CW < 64 ? CW : 64;
+#pragma unroll
+                        for (int c = 0; c < CW; c += kBox)
+                            if (n0 + c < p.N)
+                                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(&map_o),
+                                             "r"(int(n0) + c), "r"(int(m0)), "r"(tc::smem_u32(stage + c * 64))
+                                             : "memory");
+                    }
+                    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
                 }
             }
         }
         if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
+        cp_async_wait_all();
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
+    __syncwarp();
     tc::fence_before_sync();
-    __syncthreads();
-    if (warp == 1) tc::tmem_dealloc(tmem, Cfg<BN>::kTmemCols);
+    if constexpr (G == 2) cluster_sync();         // the pair's barriers and memory live until both are through
+    else __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tmem_dealloc<G>(tmem, Cf::kTmemCols);
 }
 
 // ------------------------------------------------------------- a few tokens
@@ -451,21 +599,40 @@ k_proj_fp8_few(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ wq, P
 // --------------------------------------------------------------------- host
 hyena_status_t fail(hyena_status_t st, const std::string& why) { return set_last_error_detail(st, why); }
 
-// [rows][K] bytes, box of 128 bytes x box_rows, 128-byte swizzle; what lies outside reads as zero.
-bool make_map(CUtensorMap* map, const void* base, uint64_t K, uint64_t rows, uint32_t box_rows, std::string* why) {
+bool encode(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, const void* base, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle, std::string* why) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     cudaError_t e = tensor_map_encoder(&enc);
     if (e != cudaSuccess) {
         *why = std::string("cuTensorMapEncodeTiled unavailable: ") + cudaGetErrorString(e);
         return false;
     }
-    const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
-    const cuuint32_t box[2] = {BKB, box_rows}, estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t one[3] = {1, 1, 1};
+    CUresult r = enc(map, type, rank, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) *why = "cuTensorMapEncodeTiled failed (" + std::to_string(int(r)) + ")";
     return r == CUDA_SUCCESS;
+}
+
+// [rows][K] bytes, box of 128 bytes x box_rows, 128-byte swizzle; what lies outside reads as zero.
+bool operand_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int box_rows, std::string* why) {
+    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)}, strides[1] = {cuuint64_t(K)};
+    const cuuint32_t box[2] = {BKB, cuuint32_t(box_rows)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, why);
+}
+
+// The output as it leaves: a warp's 32 rows x 64 columns at a time (channels_first: four warps' 64 positions x cw channels).
+bool output_map(CUtensorMap* map, const Params& p, int cw, std::string* why) {
+    if (p.channels_first) {
+        const cuuint64_t dims[3] = {cuuint64_t(p.L), cuuint64_t(p.N), cuuint64_t(p.M / p.L)};
+        const cuuint64_t strides[2] = {cuuint64_t(p.L) * 2, cuuint64_t(p.N * p.L) * 2};
+        const cuuint32_t box[3] = {64, cuuint32_t(cw), 1};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, why);
+    }
+    const cuuint64_t dims[2] = {cuuint64_t(p.N), cuuint64_t(p.M)}, strides[1] = {cuuint64_t(p.N) * 2};
+    const cuuint32_t box[2] = {cuuint32_t(cw < 64 ? cw : 64), 32};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, dims, strides, box,
+                  cw < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, why);
 }
 
 int sm_count() {
@@ -475,15 +642,37 @@ int sm_count() {
     return sms;
 }
 
-template <int BN>
-cudaError_t launch(const CUtensorMap& mx, const CUtensorMap& mw, Params& p, int sms, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(k_proj_fp8<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<BN>::kSmem));
-    if (e != cudaSuccess) return e;
-    p.tiles_m = int((p.M + BM - 1) / BM);
+template <int BN, int G>
+hyena_status_t launch(const void* xq, const void* wq, Params& p, int sms, cudaStream_t s) {
+    using Cf = Cfg<BN, G>;
+    std::string why;
+    CUtensorMap mx, mw, mo;
+    p.tiles_m = int((p.M + BM * G - 1) / (BM * G));
     p.tiles_n = int((p.N + BN - 1) / BN);
-    const int tiles = p.tiles_m * p.tiles_n;
-    k_proj_fp8<BN><<<unsigned(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s>>>(mx, mw, p);
-    return cudaGetLastError();
+    // whole 16-byte pieces of rows, and (channels_first) a CTA's 128 positions in one batch row
+    p.store = (p.channels_first ? p.L % 128 == 0 : p.N % 8 == 0) ? STORE_TMA : STORE_PLAIN;
+    if (!operand_map(&mx, xq, p.K, p.M, BM, &why) || !operand_map(&mw, wq, p.K, p.N, G == 2 ? BN / 4 : BN, &why)) return fail(HYENA_ERR_CUDA, why);
+    if (p.store == STORE_TMA && !output_map(&mo, p, Cf::CW, &why)) return fail(HYENA_ERR_CUDA, why);
+    if (p.store != STORE_TMA) mo = mx;            // not used
+    cudaError_t e = kernel_status_word(&p.status);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_proj_fp8<BN, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cf::kSmem));
+    if (e == cudaSuccess) {
+        const int tiles = p.tiles_m * p.tiles_n, most = sms / G;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(G * (tiles < most ? tiles : most)));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Cf::kSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {unsigned(G), 1, 1};
+        cfg.attrs = at;
+        cfg.numAttrs = G > 1 ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, k_proj_fp8<BN, G>, mx, mw, mo, p);
+    }
+    if (e != cudaSuccess) return fail(HYENA_ERR_CUDA, std::string("8-bit projection: ") + cudaGetErrorString(e));
+    return set_last_error_detail(HYENA_OK, "");
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -518,31 +707,22 @@ extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const 
         (bias && overlaps(out, no, bias, size_t(N) * 4)))
         return fail(HYENA_ERR_INVALID_ARG, "out overlaps an input");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Params p{M, L, N, K, int(kblocks), 0, 0, xs, Ws, bias, static_cast<bf16*>(out), channels_first != 0,
+    Params p{M, L, N, K, int(kblocks), 0, 0, xs, Ws, bias, static_cast<bf16*>(out), channels_first != 0, STORE_PLAIN,
              kDefaultWaitBudgetNs, nullptr};
-    cudaError_t e;
     if (M <= kFewTokens) {
         const unsigned grid = unsigned((N + 15) / 16);
         const uint8_t *x = static_cast<const uint8_t*>(xq), *w = static_cast<const uint8_t*>(Wq);
         if (M <= 8) k_proj_fp8_few<1><<<grid, kFewThreads, 0, s>>>(x, w, p);
         else if (M <= 16) k_proj_fp8_few<2><<<grid, kFewThreads, 0, s>>>(x, w, p);
         else k_proj_fp8_few<4><<<grid, kFewThreads, 0, s>>>(x, w, p);
-        e = cudaGetLastError();
-    } else {
-        // the widest tile that leaves every SM one; narrower ones spread a small product
-        const int sms = sm_count();
-        const int64_t tm = (M + BM - 1) / BM;
-        const int bn = tm * ((N + 255) / 256) >= sms ? 256 : tm * ((N + 127) / 128) >= sms ? 128 : 64;
-        std::string why;
-        CUtensorMap mx, mw;
-        if (!make_map(&mx, xq, uint64_t(K), uint64_t(M), BM, &why) || !make_map(&mw, Wq, uint64_t(K), uint64_t(N), uint32_t(bn), &why))
-            return fail(HYENA_ERR_CUDA, why);
-        e = kernel_status_word(&p.status);
-        if (e == cudaSuccess)
-            e = bn == 256   ? launch<256>(mx, mw, p, sms, s)
-                : bn == 128 ? launch<128>(mx, mw, p, sms, s)
-                            : launch<64>(mx, mw, p, sms, s);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return fail(HYENA_ERR_CUDA, std::string("8-bit projection: ") + cudaGetErrorString(e));
+        return set_last_error_detail(HYENA_OK, "");
     }
-    if (e != cudaSuccess) return fail(HYENA_ERR_CUDA, std::string("8-bit projection: ") + cudaGetErrorString(e));
-    return set_last_error_detail(HYENA_OK, "");
+    // the widest tile that leaves every SM one; narrower ones spread a small product
+    const int sms = sm_count();
+    const int64_t tm = (M + BM - 1) / BM;
+    if (tm * ((N + 255) / 256) >= sms) return launch<256, 2>(xq, Wq, p, sms, s);
+    if (tm * ((N + 127) / 128) >= sms) return launch<128, 1>(xq, Wq, p, sms, s);
+    return launch<64, 1>(xq, Wq, p, sms, s);
 }
