@@ -15,9 +15,8 @@
 //               tensor-memory buffers, a commit per block;
 //   warps 4-11  two warpgroups, half of the columns each (their sums take most
 //               of the registers, which the first warpgroup hands over): read a
-//               block's P with tcgen05.ld, free the buffer, add it times the
-//               row's factor.  A thread holds one row, so the factor is one
-//               number a block.
+//               block's P with tcgen05.ld as fragments, free the buffer, add it
+//               times the rows' factors (four rows a thread).
 // Tiles.  Large products run on pairs of CTAs (cta_group::2): 256 x 256, each
 // CTA the sums of its 128 rows and half of the W rows in its shared memory, so
 // a block brings 32 KB into an SM for its 512 cycles of tensor work; a CTA by
@@ -81,12 +80,20 @@ struct Cfg {
     static constexpr uint32_t kStageBytes = kATile + kBTile;
     static constexpr uint32_t kTmemCols = 2 * BN;
     static constexpr int CW = BN / 2;             // columns a consuming thread
-    // Pairs hand over each half of the columns by itself: a buffer's round trip (products, reading, arrivals across the
-    // pair) is longer than two blocks' products, and half as much is read in half of them.
-    static constexpr int H = G;
     static constexpr uint32_t kOutWarp = 32 * CW * 2;
     static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 8 * kOutWarp + 512 + 8 * CW * 4 + 2 * kRing * 256 * 4;
 };
+
+// Neighbouring tiles at work together lie along the output's contiguous axis.
+__device__ __forceinline__ void place(const Params& p, int tile, int& tm, int& tn) {
+    if (p.channels_first) {
+        tn = tile / p.tiles_m;
+        tm = tile - tn * p.tiles_m;
+    } else {
+        tm = tile / p.tiles_n;
+        tn = tile - tm * p.tiles_n;
+    }
+}
 
 template <int G>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -153,6 +160,35 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
     else tc::tmem_dealloc(base, cols);
 }
 
+// 16 lanes x 32 columns of tensor memory as the fragments of m16n8 products lie: of the 8 columns from 8 j thread
+// (g = lane / 4, t = lane % 4) gets row g, columns 2 t, 2 t + 1 in v[4 j], v[4 j + 1] and row g + 8 in the next two.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&r)[16]) {
+    uint32_t v[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(v[i]);
+}
+
+// Four 8 x 8 matrices of 16-bit numbers from fragments, rows as they are or transposed.
+__device__ __forceinline__ void stmatrix4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4_trans(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(one));
+    return one != 0;
+}
+
 // acc += v f on pairs (one instruction for two fp32 multiply-adds)
 __device__ __forceinline__ void fma2(uint64_t& acc, float v0, float v1, uint64_t f2) {
     uint64_t v2;
@@ -171,16 +207,15 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     using Cf = Cfg<BN, G>;
     constexpr int kStages = Cf::kStages;
     constexpr uint32_t kStageBytes = Cf::kStageBytes;
-    constexpr int CW = Cf::CW, H = Cf::H;
+    constexpr int CW = Cf::CW;
     extern __shared__ __align__(1024) uint8_t smem_p[];
     // the same offset in both CTAs of a pair: the base is the kernel's own in each
     uint8_t* stages = smem_p + ((1024u - (tc::smem_u32(smem_p) & 1023u)) & 1023u);
     uint8_t* out_stage = stages + kStages * kStageBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + 8 * Cf::kOutWarp);
-    uint64_t* empty = full + kStages;
-    uint64_t* acc_full = empty + kStages;         // [half][buffer]
-    uint64_t* acc_empty = acc_full + 4;
-    uint64_t* out_full = acc_empty + 4;           // [half]: its four warps have staged their part
+    uint64_t* done = full + kStages;              // a stage's products: it is free, and its sums are there
+    uint64_t* acc_empty = done + kStages;         // [buffer]
+    uint64_t* out_full = acc_empty + 2;           // [half]: its four warps have staged their part
     uint64_t* out_free = out_full + 2;            // [half]: the staging has been read
     uint64_t* mma_done = out_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -193,13 +228,10 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], 1);
-        }
-        for (int a = 0; a < 4; ++a) {
-            tc::mbar_init(&acc_full[a], 1);
-            tc::mbar_init(&acc_empty[a], 8 / H * G);               // one arrival a reading warp
+            tc::mbar_init(&done[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(&acc_empty[a], 8 * G);  // one arrival a reading warp
             tc::mbar_init(&out_full[a], 4);
             tc::mbar_init(&out_free[a], 1);
         }
@@ -219,13 +251,14 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         // one thread each: stage and buffer counters step, nothing is divided, so that issuing stays under the products
         if (warp == 0 && lane == 0) {
             int s = 0, issued = 0;
-            uint32_t phase = 1;                   // of `empty`: the first round finds the stages free
+            uint32_t phase = 1;                   // of `done`: the first round finds the stages free
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
-                const int tm = tile / p.tiles_n;
-                const int m0 = (tm * G + rank) * BM, n0 = (tile - tm * p.tiles_n) * BN;
+                int tm, tn;
+                place(p, tile, tm, tn);
+                const int m0 = (tm * G + rank) * BM, n0 = tn * BN + rank * (BN / 2);
                 for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (!tc::mbar_wait(&empty[s], phase, p.budget_ns)) {
+                    if (!tc::mbar_wait(&done[s], phase, p.budget_ns)) {
                         ok = false;
                         break;
                     }
@@ -234,10 +267,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         // the first CTA's barrier counts the bytes of both
                         if (rank == 0) tc::mbar_expect_tx(&full[s], 2 * kStageBytes);
                         tma_load_pair(sa, &map_x, kb * BKB, m0, &full[s]);
-                        // each CTA holds half of the W rows of each half of the columns
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_pair(sa + kATile + h * (BN / 4) * BKB, &map_w, kb * BKB, n0 + h * CW + rank * (BN / 4), &full[s]);
+                        tma_load_pair(sa + kATile, &map_w, kb * BKB, n0, &full[s]);
                     } else {
                         tc::mbar_expect_tx(&full[s], kStageBytes);
                         tc::tma_load_2d(sa, &map_x, kb * BKB, m0, &full[s]);
@@ -258,39 +288,38 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     phase ^= 1u;
                 }
                 --s;
-                if constexpr (G == 2) tc::mbar_wait(&empty[s], phase ^ 1u, p.budget_ns);
+                if constexpr (G == 2) tc::mbar_wait(&done[s], phase ^ 1u, p.budget_ns);
                 else tc::mbar_wait(&full[s], phase ^ 1u, p.budget_ns);
             }
             // the second CTA of a pair stays until the last arrival at its barriers
             if (rank == 1) tc::mbar_wait(mma_done, 0, p.budget_ns);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(BM * G, BN / H);
+        } else if (warp == 1 && rank == 0) {
+            // the whole warp walks the loop, so that descriptors stay in uniform registers; one lane issues
+            constexpr uint32_t idesc = idesc_e4m3(BM * G, BN);
             const uint64_t da0 = tc::desc_sw128(tc::smem_u32(stages), 16, 1024), db0 = da0 + (kATile >> 4);
             const int tail = int((p.K - int64_t(p.kblocks - 1) * BKB + 31) / 32);     // products of the last block
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 1;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
-                for (int kb = 0; kb < p.kblocks && ok; ++kb) {
-                    ok = tc::mbar_wait(&full[s], phase, p.budget_ns);
-                    const uint64_t da = da0 + uint32_t(s) * (kStageBytes >> 4);
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    if (!tc::mbar_wait(&full[s], phase, p.budget_ns) || !tc::mbar_wait(&acc_empty[acc], acc_phase, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t da = da0 + uint32_t(s) * (kStageBytes >> 4), db = db0 + uint32_t(s) * (kStageBytes >> 4);
+                    const uint32_t d = tmem + uint32_t(acc) * BN;
                     // the tail of the last block lies behind K: zeros, and no products for whole steps of them
                     const int steps = kb + 1 < p.kblocks ? 4 : tail;
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        ok = ok && tc::mbar_wait(&acc_empty[2 * h + acc], acc_phase, p.budget_ns);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        const uint64_t db = db0 + uint32_t(s) * (kStageBytes >> 4) + h * ((BN / 4 * BKB) >> 4);
-                        const uint32_t d = tmem + uint32_t(acc) * BN + h * CW;
+                    if (elect_one()) {
                         mma_e4m3<G>(d, da, db, idesc, 0u);
                         if (steps > 1) mma_e4m3<G>(d, da + 2, db + 2, idesc, 1u);
                         if (steps > 2) mma_e4m3<G>(d, da + 4, db + 4, idesc, 1u);
                         if (steps > 3) mma_e4m3<G>(d, da + 6, db + 6, idesc, 1u);
-                        commit<G>(&acc_full[2 * h + acc]);
+                        commit<G>(&done[s]);
                     }
-                    if (!ok) break;
-                    commit<G>(&empty[s]);
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1u;
@@ -299,29 +328,30 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     acc_phase ^= acc == 0;
                 }
             }
-            if (!ok) report_status(p.status, kStatusTimeout);
+            if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
             // nothing left in flight before tensor memory is released
-            commit<G>(mma_done);
-            if (!tc::mbar_wait(mma_done, 0, p.budget_ns)) report_status(p.status, kStatusTimeout);
+            if (elect_one()) commit<G>(mma_done);
+            __syncwarp();
+            if (!tc::mbar_wait(mma_done, 0, p.budget_ns) && lane == 0) report_status(p.status, kStatusTimeout);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t t_col = tmem + uint32_t(half * CW) + (uint32_t(32 * q) << 16);
         uint8_t* stage = out_stage + (warp - 4) * Cf::kOutWarp;     // (channels_first: a half's four parts together)
-        uint64_t *my_full = acc_full + (H == 2 ? 2 * half : 0), *my_empty = acc_empty + (H == 2 ? 2 * half : 0);
         float* bias = s_bias + (warp - 4) * CW;
         // The scales come kAhead blocks ahead (a block's products take less than a load under traffic), across tiles, by
-        // asynchronous 4-byte copies into a ring of this thread's own slots.
-        float2* ring = reinterpret_cast<float2*>(s_ring) + (int(threadIdx.x) - 128);
+        // asynchronous 4-byte copies into a ring of the warp's own, row `lane` by this lane.
+        float2* ring = reinterpret_cast<float2*>(s_ring) + 32 * (warp - 4);
         int pt = first, pc = 0, pkb = p.kblocks;  // the tile, the ring's slot and the block to fetch next
         const float *px = nullptr, *pw = nullptr;
         bool plive = false;
         auto fetch = [&]() {
             if (pkb == p.kblocks) {               // enter tile pt
-                const int tm = pt / p.tiles_n;
+                int tm, tn;
+                place(p, pt, tm, tn);
                 const uint32_t m = (uint32_t(tm) * G + rank) * BM + 32 * q + lane;
-                const int64_t n = int64_t(pt - tm * p.tiles_n) * BN + half * CW;
+                const int64_t n = int64_t(tn) * BN + half * CW;
                 plive = pt < tiles && m < p.M && n < p.N;
                 const int64_t b = plive ? m / uint32_t(p.L) : 0;
                 px = p.xs + b * (p.kblocks - 1) * p.L + (plive ? m : 0);
@@ -330,8 +360,8 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 pkb = 0;
             }
             if (plive) {
-                cp_async_small<4>(&ring[pc].x, px);
-                cp_async_small<4>(&ring[pc].y, pw);
+                cp_async_small<4>(&ring[pc + lane].x, px);
+                cp_async_small<4>(&ring[pc + lane].y, pw);
             }
             cp_async_commit();
             px += p.L;
@@ -341,58 +371,73 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         };
 #pragma unroll 1
         for (int i = 0; i < kAhead; ++i) fetch();
-        int buf = 0, slot = 0;
+        int buf = 0, slot = 0, s = 0;
         uint32_t phase = 0, out_phase = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
-            const int tm = tile / p.tiles_n;
+            int tm, tn;
+            place(p, tile, tm, tn);
             const int64_t m0 = (int64_t(tm) * G + rank) * BM + 32 * q, m = m0 + lane;
-            const int64_t n0 = int64_t(tile - tm * p.tiles_n) * BN + half * CW;
-            const bool live = m < p.M, row_in = live && n0 < p.N;
+            const int64_t n0 = int64_t(tn) * BN + half * CW;
+            const bool live = m < p.M;
             const int64_t b = live ? uint32_t(m) / uint32_t(p.L) : 0, l = live ? m - b * p.L : 0;
             // the bias of this warp's columns, its own copy: no barrier that a warp which gave up would leave others at
             __syncwarp();
 #pragma unroll
             for (int i = lane; i < CW; i += 32) bias[i] = (p.bias && n0 + i < p.N) ? __ldg(p.bias + n0 + i) : 0.0f;
             __syncwarp();
-            uint64_t acc[CW / 2];                 // pairs of neighbouring columns
+            // sums as pairs of neighbouring columns: of rows g + 16 hh and g + 8 + 16 hh, columns 8 j + 2 t
+            uint64_t acc[2][CW / 8][2];
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < CW / 2; ++i) (&acc[0][0][0])[i] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < p.kblocks; ++kb) {
-                if (!tc::mbar_wait(&my_full[buf], phase, p.budget_ns)) {
+                if (!tc::mbar_wait(&done[s], phase, p.budget_ns)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                // 16 columns load under the multiply-adds of 16, the first while the factor comes
+                // a piece of 16 rows x 32 columns loads under the multiply-adds of another, the first while the factors come
+                constexpr int kPieces = CW / 16;
                 float v[2][16];
-                tc::tmem_ld16(t_col + uint32_t(buf * BN), v[0]);
+                tmem_ld_frag(t_col + uint32_t(buf * BN), v[0]);
                 asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
-                const float2 sc = ring[slot];
-                const float f = row_in ? sc.x * sc.y : 0.0f;
-                uint64_t f2;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+                __syncwarp();
+                uint64_t f2[4];                   // of rows g + 8 i
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 sc = ring[slot + (lane >> 2) + 8 * i];
+                    const float f = m0 + (lane >> 2) + 8 * i < p.M && n0 < p.N ? sc.x * sc.y : 0.0f;
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(f2[i]) : "f"(f));
+                }
                 slot = (slot + 256) & (kRing * 256 - 1);
                 fetch();
 #pragma unroll
-                for (int c = 0; c < CW / 16; ++c) {
+                for (int c = 0; c < kPieces; ++c) {
                     tc::tmem_ld_wait();
-                    if (c + 1 < CW / 16) {
-                        tc::tmem_ld16(t_col + uint32_t(buf * BN + 16 * (c + 1)), v[(c + 1) & 1]);
+                    if (c + 1 < kPieces) {
+                        const int hh = (c + 1) / (CW / 32), cc = (c + 1) % (CW / 32);
+                        tmem_ld_frag(t_col + uint32_t(buf * BN + 32 * cc) + (uint32_t(16 * hh) << 16), v[(c + 1) & 1]);
                     } else {
                         tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) {
-                            if constexpr (G == 2) arrive_first(&my_empty[buf]);
-                            else tc::mbar_arrive(&my_empty[buf]);
+                            if constexpr (G == 2) arrive_first(&acc_empty[buf]);
+                            else tc::mbar_arrive(&acc_empty[buf]);
                         }
                     }
+                    const int hh = c / (CW / 32), cc = c % (CW / 32);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f2);
+                    for (int j = 0; j < 4; ++j) {
+                        fma2(acc[hh][4 * cc + j][0], v[c & 1][4 * j], v[c & 1][4 * j + 1], f2[2 * hh]);
+                        fma2(acc[hh][4 * cc + j][1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3], f2[2 * hh + 1]);
+                    }
                 }
                 buf ^= 1;
-                phase ^= buf == 0;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
             if (!ok) {                            // a wait ran out: NaN for this row's outputs
                 for (int i = 0; live && i < CW && n0 + i < p.N; ++i)
@@ -411,50 +456,44 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     break;
                 }
             }
-            if (p.channels_first) {
-                if (p.store == STORE_TMA) {
-                    // [64 positions' box][column][64 positions], 128-byte swizzle.  Lanes are neighbouring positions: of two
-                    // columns four apart an even lane takes the pair of the first, an odd one that of the second (four
-                    // apart, their pieces lie on different halves of the banks).
-                    uint8_t* so = out_stage + half * (4 * Cf::kOutWarp) + (q >> 1) * (CW * 128) + (lane & 1) * (4 * 128) + ((lane >> 1) & 3) * 4;
-                    const int piece = 4 * (q & 1) + (lane >> 3), odd = (lane & 1) * 4;
+            // The staging.  channels_first: the half's [64 positions' box][column][64 positions]; else the warp's [box of kBox
+            // columns][row][kBox columns]; 128-byte swizzle (64-byte rows: 64-byte swizzle).
+            constexpr int kBox = CW < 64 ? CW : 64;
+            uint8_t* half_stage = out_stage + half * (4 * Cf::kOutWarp);
+            const int mat = lane >> 3, mr = lane & 7;
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) {
-                        if (i & 4) continue;
-                        const float2 a = unpair(acc[i / 2]), e = unpair(acc[(i + 4) / 2]);
-                        const float x = ((i & 1) ? a.y : a.x) + bias[i], y = ((i & 1) ? e.y : e.x) + bias[i + 4];
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
-                        *reinterpret_cast<uint32_t*>(so + i * 128 + 16 * (piece ^ ((i + odd) & 7))) =
-                            (lane & 1) ? tc::pack2(other, y) : tc::pack2(x, other);
-                    }
-                } else {
-                    bf16* o = p.out + (b * p.N + n0) * p.L + l;
+            for (int j = 0; j < CW / 8; j += 2) {
+                const float2 b0 = *reinterpret_cast<const float2*>(bias + 8 * j + 2 * (lane & 3));
+                const float2 b1 = *reinterpret_cast<const float2*>(bias + 8 * j + 8 + 2 * (lane & 3));
 #pragma unroll
-                    for (int i = 0; i < CW; i += 2) {
-                        const float2 a = unpair(acc[i / 2]), bb = *reinterpret_cast<const float2*>(bias + i);
-                        if (live && n0 + i < p.N) o[0] = __float2bfloat16_rn(a.x + bb.x);
-                        if (live && n0 + i + 1 < p.N) o[p.L] = __float2bfloat16_rn(a.y + bb.y);
-                        o += 2 * p.L;
-                    }
-                }
-            } else {
-                // row `lane` of the warp's 32: in boxes of 64 columns, 128-byte swizzle (of 32, 64-byte swizzle)
-                constexpr int kBox = CW < 64 ? CW : 64;
-#pragma unroll
-                for (int j = 0; j < CW / 8; ++j) {
+                for (int hh = 0; hh < 2; ++hh) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 a = unpair(acc[4 * j + i]);
-                        const float2 bb = *reinterpret_cast<const float2*>(bias + 8 * j + 2 * i);
+                        const float2 a = unpair(acc[hh][j + (i >> 1)][i & 1]), bb = i < 2 ? b0 : b1;
                         w[i] = tc::pack2(a.x + bb.x, a.y + bb.y);
                     }
-                    const int box = j / (kBox / 8), c = j % (kBox / 8);
-                    const int at = kBox == 64 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
-                    *reinterpret_cast<uint4*>(stage + box * (32 * kBox * 2) + lane * (kBox * 2) + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    // matrix `mat`: rows 16 hh + 8 (mat & 1) .., columns 8 (j + (mat >> 1)) ..
+                    if (p.channels_first) {
+                        const int n = 8 * (j + (mat >> 1)) + mr, piece = 4 * (q & 1) + 2 * hh + (mat & 1);
+                        stmatrix4_trans(tc::smem_u32(half_stage) + (q >> 1) * (CW * 128) + n * 128 + 16 * (piece ^ (n & 7)), w[0], w[1], w[2], w[3]);
+                    } else {
+                        const int r = 16 * hh + 8 * (mat & 1) + mr, cg = j + (mat >> 1), box = cg / (kBox / 8), c = cg % (kBox / 8);
+                        const int at = kBox == 64 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                        stmatrix4(tc::smem_u32(stage) + box * (32 * kBox * 2) + r * (kBox * 2) + 16 * at, w[0], w[1], w[2], w[3]);
+                    }
                 }
-                if (p.store == STORE_PLAIN) {
-                    __syncwarp();
+            }
+            if (p.store == STORE_PLAIN) {
+                __syncwarp();
+                if (p.channels_first) {
+                    bf16* o = p.out + (b * p.N + n0) * p.L + l;
+                    const uint8_t* so = half_stage + (q >> 1) * (CW * 128) + 2 * (lane & 7);
+                    const int piece = 4 * (q & 1) + (lane >> 3);
+#pragma unroll 8
+                    for (int n = 0; n < CW; ++n)
+                        if (live && n0 + n < p.N) o[int64_t(n) * p.L] = *reinterpret_cast<const bf16*>(so + n * 128 + 16 * (piece ^ (n & 7)));
+                } else {
 #pragma unroll 4
                     for (int i = lane; i < 32 * CW; i += 32) {
                         const int r = i / CW, n = i % CW, box = n / kBox, c = (n % kBox) / 8;
@@ -462,8 +501,8 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                         const bf16 w = *reinterpret_cast<const bf16*>(stage + box * (32 * kBox * 2) + r * (kBox * 2) + 16 * at + 2 * (n & 7));
                         if (m0 + r < p.M && n0 + n < p.N) p.out[(m0 + r) * p.N + n0 + n] = w;
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
             }
             if (p.store == STORE_TMA) {
                 tc::fence_proxy_async();
@@ -485,7 +524,6 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                                          "r"(tc::smem_u32(stage + c * (CW * 128)))
                                          : "memory");
                     } else {
-                        constexpr int kBox = CW < 64 ? CW : 64;
 #pragma unroll
                         for (int c = 0; c < CW; c += kBox)
                             if (n0 + c < p.N)
@@ -651,7 +689,7 @@ hyena_status_t launch(const void* xq, const void* wq, Params& p, int sms, cudaSt
     p.tiles_n = int((p.N + BN - 1) / BN);
     // whole 16-byte pieces of rows, and (channels_first) a CTA's 128 positions in one batch row
     p.store = (p.channels_first ? p.L % 128 == 0 : p.N % 8 == 0) ? STORE_TMA : STORE_PLAIN;
-    if (!operand_map(&mx, xq, p.K, p.M, BM, &why) || !operand_map(&mw, wq, p.K, p.N, G == 2 ? BN / 4 : BN, &why)) return fail(HYENA_ERR_CUDA, why);
+    if (!operand_map(&mx, xq, p.K, p.M, BM, &why) || !operand_map(&mw, wq, p.K, p.N, BN / G, &why)) return fail(HYENA_ERR_CUDA, why);
     if (p.store == STORE_TMA && !output_map(&mo, p, Cf::CW, &why)) return fail(HYENA_ERR_CUDA, why);
     if (p.store != STORE_TMA) mo = mx;            // not used
     cudaError_t e = kernel_status_word(&p.status);
