@@ -287,18 +287,27 @@ class DeltaRule(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("state_in", "state_out", "lengths")])
 
 
-def _on_device(*tensors) -> None:
-    """The kernels run on the current device: its own tensors only."""
+def _on_device(*tensors) -> int:
+    """The kernels run on the current device: its own tensors only (None passes)."""
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; of the device's current stream without an object around it."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _plain(name, t, shape, dtype) -> None:
     """A contiguous tensor of this shape and dtype (None passes)."""
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -309,21 +318,19 @@ def _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, three) -> Delt
     if Hk < 1 or Hv < 1 or q.shape[1] % Hk or v.shape[1] % Hv:
         raise ValueError("the channels of q and k must divide into Hk heads, those of v into Hv")
     dk, dv = q.shape[1] // Hk, v.shape[1] // Hv
-    tail = (L,) if three else ()
-    for name, t, c in (("q", q, Hk * dk), ("k", k, Hk * dk), ("v", v, Hv * dv), ("o", o, Hv * dv)):
-        if tuple(t.shape) != (B, c) + tail or t.dtype != q.dtype:
-            raise ValueError(f"{name} must be {q.dtype} {(B, c) + tail}, got {t.dtype} {tuple(t.shape)}")
+    ck, cv, heads = ((B, Hk * dk, L), (B, Hv * dv, L), (B, Hv, L)) if three else ((B, Hk * dk), (B, Hv * dv), (B, Hv))
+    dtype = q.dtype
+    for name, t, c in (("q", q, ck), ("k", k, ck), ("v", v, cv), ("o", o, cv)):
+        if t.shape != c or t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} {c}, got {t.dtype} {tuple(t.shape)}")
     for name, t in (("g", g), ("beta", beta)):
-        if t is not None and (tuple(t.shape) != (B, Hv) + tail or t.dtype != torch.float32):
-            raise ValueError(f"{name} must be float32 {(B, Hv) + tail}, got {t.dtype} {tuple(t.shape)}")
-    i3 = ctypes.c_int64 * 3
-
-    def stride(t):                                   # two strides: the third, of the one token, stays 0
-        return i3(*t.stride()) if t is not None else i3()
-
+        if t is not None and (t.shape != heads or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be float32 {heads}, got {t.dtype} {tuple(t.shape)}")
+    none = (0, 0, 0)                                  # without the third (one token): stays 0
     return DeltaRule(B, L, Hk, Hv, dk, dv, _dtype_code(q), HYENA_DELTA_L2NORM if l2norm else 0,
-                     0.0 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(g),
-                     _ptr(beta), stride(q), stride(k), stride(v), stride(o), stride(g), stride(beta))
+                     0.0 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                     None if g is None else g.data_ptr(), None if beta is None else beta.data_ptr(), q.stride(), k.stride(),
+                     v.stride(), o.stride(), none if g is None else g.stride(), none if beta is None else beta.stride())
 
 
 def hyena_delta_rule_workspace_bytes(B: int, L: int, Hk: int, Hv: int, dk: int, dv: int, dtype) -> int:
@@ -341,7 +348,7 @@ def hyena_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in=None, state
     lengths: [B] int32 or None, workspace: uint8 of
     hyena_delta_rule_workspace_bytes(...) or None when that is 0."""
     import torch
-    _on_device(q, k, v, g, beta, o, state_in, state_out, lengths, workspace)
+    dev = _on_device(q, k, v, g, beta, o, state_in, state_out, lengths, workspace)
     B, _, L = q.shape
     a = _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, True)
     _plain("state_in", state_in, (B, Hv, a.dk, a.dv), torch.float32)
@@ -349,7 +356,7 @@ def hyena_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in=None, state
     _plain("lengths", lengths, (B,), torch.int32)
     a.state_in, a.state_out, a.lengths = _ptr(state_in), _ptr(state_out), _ptr(lengths)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().hyena_delta_rule(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream(stream)))
+    _check(load().hyena_delta_rule(ctypes.byref(a), _ptr(workspace), ws_bytes, _raw_stream(stream, dev)))
 
 
 def hyena_delta_rule_step(q, k, v, g, beta, o, states, Hk: int, Hv: int, slots=None, scale=None, l2norm: bool = False,
@@ -358,45 +365,45 @@ def hyena_delta_rule_step(q, k, v, g, beta, o, states, Hk: int, Hv: int, slots=N
     None, states: [n, Hv, dk, dv] f32 updated in place, slots: [B] int32 (row b
     uses state slots[b], negative: padding) or None (row b uses state b)."""
     import torch
-    _on_device(q, k, v, g, beta, o, states, slots)
+    dev = _on_device(q, k, v, g, beta, o, states, slots)
     B = q.shape[0]
     a = _delta_args(q, k, v, g, beta, o, B, 1, Hk, Hv, scale, l2norm, False)
     _plain("states", states, (states.shape[0], Hv, a.dk, a.dv), torch.float32)
     _plain("slots", slots, (B,), torch.int32)
     _check(load().hyena_delta_rule_step(ctypes.byref(a), states.data_ptr(), states.shape[0], _ptr(slots),
-                                        _stream(stream)))
+                                        _raw_stream(stream, dev)))
 
 
 def hyena_quantize_fp8(x, xq, xs, channels_first: bool = False, stream=None) -> None:
     """x [B, L, K] (or [B, K, L] with channels_first) f32 or bf16 -> xq [B, L, K]
     float8_e4m3fn, xs [B, ceil(K/128), L] f32."""
     import torch
-    _on_device(x, xq, xs)
+    dev = _on_device(x, xq, xs)
     B, L, K = (x.shape[0], x.shape[2], x.shape[1]) if channels_first else x.shape
-    _plain("x", x, tuple(x.shape), x.dtype)
+    _plain("x", x, x.shape, x.dtype)
     _plain("xq", xq, (B, L, K), torch.float8_e4m3fn)
     _plain("xs", xs, (B, -(-K // 128), L), torch.float32)
     _check(load().hyena_quantize_fp8(x.data_ptr(), xq.data_ptr(), xs.data_ptr(), B, L, K, _dtype_code(x),
-                                     1 if channels_first else 0, _stream(stream)))
+                                     1 if channels_first else 0, _raw_stream(stream, dev)))
 
 
 def hyena_quantize_fp8_weight(W, Wq, Ws, stream=None) -> None:
     """W [N, K] f32 or bf16 -> Wq [N, K] float8_e4m3fn, Ws [ceil(N/128), ceil(K/128)] f32."""
     import torch
-    _on_device(W, Wq, Ws)
+    dev = _on_device(W, Wq, Ws)
     N, K = W.shape
     _plain("W", W, (N, K), W.dtype)
     _plain("Wq", Wq, (N, K), torch.float8_e4m3fn)
     _plain("Ws", Ws, (-(-N // 128), -(-K // 128)), torch.float32)
     _check(load().hyena_quantize_fp8_weight(W.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), N, K, _dtype_code(W),
-                                            _stream(stream)))
+                                            _raw_stream(stream, dev)))
 
 
 def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stream=None) -> None:
     """xq [B, L, K], Wq [N, K] float8_e4m3fn with their scales, bias [N] f32 or
     None -> out bf16 [B, L, N], or [B, N, L] with channels_first."""
     import torch
-    _on_device(xq, xs, Wq, Ws, bias, out)
+    dev = _on_device(xq, xs, Wq, Ws, bias, out)
     B, L, K = xq.shape
     N = Wq.shape[0]
     _plain("xq", xq, (B, L, K), torch.float8_e4m3fn)
@@ -406,7 +413,7 @@ def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stre
     _plain("bias", bias, (N,), torch.float32)
     _plain("out", out, (B, N, L) if channels_first else (B, L, N), torch.bfloat16)
     _check(load().hyena_proj_fp8(xq.data_ptr(), xs.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), _ptr(bias),
-                                 out.data_ptr(), B, L, K, N, 1 if channels_first else 0, _stream(stream)))
+                                 out.data_ptr(), B, L, K, N, 1 if channels_first else 0, _raw_stream(stream, dev)))
 
 
 def hyena_kernel_status(stream=None) -> None:

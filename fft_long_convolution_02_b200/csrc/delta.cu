@@ -183,7 +183,7 @@ cudaError_t launch_seq_t(const DeltaArgs& a, cudaStream_t s) {
 constexpr int kStepThreads = 256, kStepCols = 32;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, 5)
 k_delta_step(DeltaArgs a, float* __restrict__ states, int64_t n_states, const int32_t* __restrict__ slots,
              uint32_t* status) {
     constexpr int CG = kStepCols / V;              // threads along a row of 32 columns

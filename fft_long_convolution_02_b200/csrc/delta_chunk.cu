@@ -170,6 +170,7 @@ struct ChunkArgs {
     int vec_k, vec_q, vec_v, vec_o;                // rows may be read (written) 16 bytes at a time
     uint64_t budget_ns;
     uint32_t* status;
+    int dev, sms;
 };
 
 __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
@@ -877,7 +878,8 @@ bool vec_ok(const void* p, const DeltaView& s, bool first, int head_channels) {
 template <int DK, bool FIRST>
 cudaError_t launch_prep(const ChunkArgs& x, cudaStream_t s) {
     const size_t bytes = sizeof(PrepSmem<DK, FIRST>);
-    cudaError_t e = cudaFuncSetAttribute(k_delta_prep<DK, FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    static std::atomic<bool> raised[kMaxDevices];
+    cudaError_t e = raise_smem(k_delta_prep<DK, FIRST>, bytes, x.dev, raised);
     if (e != cudaSuccess) return e;
     k_delta_prep<DK, FIRST><<<dim3(unsigned(x.chunks), unsigned(x.a.Hv), unsigned(x.a.B)), kPrepThreads, bytes, s>>>(x);
     return cudaGetLastError();
@@ -886,7 +888,8 @@ cudaError_t launch_prep(const ChunkArgs& x, cudaStream_t s) {
 template <int DK, int NW, bool FIRST>
 cudaError_t launch_scan(const ChunkArgs& x, cudaStream_t s) {
     const size_t bytes = sizeof(ScanSmem<DK, NW>);
-    cudaError_t e = cudaFuncSetAttribute(k_delta_scan<DK, NW, FIRST>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    static std::atomic<bool> raised[kMaxDevices];
+    cudaError_t e = raise_smem(k_delta_scan<DK, NW, FIRST>, bytes, x.dev, raised);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned((x.a.dv + 16 * NW - 1) / (16 * NW)), unsigned(x.a.Hv), unsigned(x.a.B));
     k_delta_scan<DK, NW, FIRST><<<grid, 32 * NW + kLoaders, bytes, s>>>(x);
@@ -899,7 +902,7 @@ cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // four warps have a scheduler each; eight share them, which pays once half-width CTAs would not all be resident
     const int64_t ctas = x.a.B * x.a.Hv * ((x.a.dv + 63) / 64);
-    return ctas <= 148 ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
+    return ctas <= x.sms ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
 }
 
 }  // namespace
@@ -913,6 +916,8 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* st
     x.chunks = int((a.L + C - 1) / C);
     x.budget_ns = kDefaultWaitBudgetNs;
     x.status = status;
+    cudaError_t e = device_sms(&x.dev, &x.sms);
+    if (e != cudaSuccess) return e;
     // the tiles lie as the keys do: along time where that is their contiguous axis
     const bool first = a.ks.st == 1 || a.ks.sc != 1;
     x.vec_k = vec_ok(a.k, a.ks, first, a.dk);

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "plan.h"
 
 namespace hyena {
@@ -22,6 +24,19 @@ constexpr uint32_t kStatusBadSlot = 4u;            // a state slot out of range,
 
 // Device address of this device's kernel status word (looked up once per device).
 cudaError_t kernel_status_word(uint32_t** out);
+
+// SMs of the current device, and its index, looked up once per device (status.cu).
+cudaError_t device_sms(int* dev, int* sms);
+
+// A kernel's dynamic shared memory limit, raised once per device; `done` is the kernel's own, one flag a device.
+constexpr int kMaxDevices = 64;
+template <typename Kernel>
+cudaError_t raise_smem(Kernel kernel, size_t bytes, int dev, std::atomic<bool> (&done)[kMaxDevices]) {
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // Records a kernel-detected condition in the status word (one thread per CTA).
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t bit) {

@@ -673,16 +673,10 @@ bool output_map(CUtensorMap* map, const Params& p, int cw, std::string* why) {
                   cw < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, why);
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 template <int BN, int G>
-hyena_status_t launch(const void* xq, const void* wq, Params& p, int sms, cudaStream_t s) {
+hyena_status_t launch(const void* xq, const void* wq, Params& p, int dev, int sms, cudaStream_t s) {
     using Cf = Cfg<BN, G>;
+    static std::atomic<bool> raised[kMaxDevices];
     std::string why;
     CUtensorMap mx, mw, mo;
     p.tiles_m = int((p.M + BM * G - 1) / (BM * G));
@@ -694,7 +688,7 @@ hyena_status_t launch(const void* xq, const void* wq, Params& p, int sms, cudaSt
     if (p.store != STORE_TMA) mo = mx;            // not used
     cudaError_t e = kernel_status_word(&p.status);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_proj_fp8<BN, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cf::kSmem));
+        e = raise_smem(k_proj_fp8<BN, G>, Cf::kSmem, dev, raised);
     if (e == cudaSuccess) {
         const int tiles = p.tiles_m * p.tiles_n, most = sms / G;
         cudaLaunchConfig_t cfg = {};
@@ -758,9 +752,11 @@ extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const 
         return set_last_error_detail(HYENA_OK, "");
     }
     // the widest tile that leaves every SM one; narrower ones spread a small product
-    const int sms = sm_count();
+    int dev = 0, sms = 0;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e != cudaSuccess) return fail(HYENA_ERR_CUDA, std::string("device: ") + cudaGetErrorString(e));
     const int64_t tm = (M + BM - 1) / BM;
-    if (tm * ((N + 255) / 256) >= sms) return launch<256, 2>(xq, Wq, p, sms, s);
-    if (tm * ((N + 127) / 128) >= sms) return launch<128, 1>(xq, Wq, p, sms, s);
-    return launch<64, 1>(xq, Wq, p, sms, s);
+    if (tm * ((N + 255) / 256) >= sms) return launch<256, 2>(xq, Wq, p, dev, sms, s);
+    if (tm * ((N + 127) / 128) >= sms) return launch<128, 1>(xq, Wq, p, dev, sms, s);
+    return launch<64, 1>(xq, Wq, p, dev, sms, s);
 }

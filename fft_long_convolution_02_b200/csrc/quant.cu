@@ -30,23 +30,29 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 
 // The scale of a block and what its quotients need.  x / s to nearest is
 // x r, corrected by its remainder (P. Markstein's division from a correctly
-// rounded reciprocal r; the remainder is exact in a fused multiply-add).  Below
-// 2^-60 the remainder could underflow: the division itself there, as for a
-// scale that is not finite.
+// rounded reciprocal r; the remainder is exact in a fused multiply-add).  For
+// largest magnitudes below 2^-50 the remainder could underflow: the division
+// itself there, as for what is not finite.
+__device__ __forceinline__ float divided(float x, float by, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, by, x), r, q);
+}
 struct Scale {
     float s, r;
     bool plain;
     __device__ __forceinline__ explicit Scale(uint32_t amax_bits) {
-        s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
-        s = s < 1.17549435e-38f ? 1.17549435e-38f : s;
+        const float m = __uint_as_float(amax_bits);
+        // 2^-50 <= m < infinity: m / 448 and every quotient by it
+        plain = amax_bits >= 0x26800000u && amax_bits < 0x7f800000u;
+        if (plain) {
+            s = divided(m, 448.0f, 1.0f / 448.0f);
+        } else {
+            s = __fdiv_rn(m, 448.0f);
+            s = s < 1.17549435e-38f ? 1.17549435e-38f : s;
+        }
         r = __frcp_rn(s);
-        plain = s >= 8.67361738e-19f && s < __int_as_float(0x7f800000);
     }
-    __device__ __forceinline__ float quotient(float x) const {
-        if (!plain) return __fdiv_rn(x, s);
-        const float q = x * r;
-        return fmaf(fmaf(-q, s, x), r, q);
-    }
+    __device__ __forceinline__ float quotient(float x) const { return plain ? divided(x, s, r) : __fdiv_rn(x, s); }
 };
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -55,21 +61,36 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
-// Eight consecutive values (16 bytes of bf16, 32 of fp32; 16-byte aligned).
-__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight consecutive values as they lie (16 bytes of bf16, 32 of fp32; 16-byte aligned).
+template <typename T>
+struct Octet;
+template <>
+struct Octet<bf16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const bf16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+};
+template <>
+struct Octet<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
 
 __device__ __forceinline__ uint2 quotients8(const Scale& sc, const float (&v)[8]) {
     return make_uint2(e4m3x4(sc.quotient(v[0]), sc.quotient(v[1]), sc.quotient(v[2]), sc.quotient(v[3])),
@@ -82,34 +103,32 @@ __device__ __forceinline__ uint2 quotients8(const Scale& sc, const float (&v)[8]
 constexpr int kRowsLast = 64;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
 k_quant_last(const T* __restrict__ x, uint8_t* __restrict__ xq, float* __restrict__ xs, int64_t L, int64_t K) {
     constexpr int kIter = kRowsLast / (kThreads / 16);
     __shared__ float s_scale[kRowsLast];
     const int64_t kb = blockIdx.x, l0 = int64_t(blockIdx.y) * kRowsLast, b = blockIdx.z;
     const int g = int(threadIdx.x) >> 4, lane = int(threadIdx.x) & 15;
     const int64_t c = kb * kBlk + lane * 8;
-    float v[kIter][8];
+    Octet<T> w[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
         const int64_t l = l0 + g + 16 * i;
-        if (l < L && c < K) {
-            load8(x + (b * L + l) * K + c, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        }
+        if (l < L && c < K) w[i].load(x + (b * L + l) * K + c);
+        else w[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
+        float v[8];
+        w[i].get(v);
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
         const Scale sc(m);
         const int64_t l = l0 + g + 16 * i;
-        if (l < L && c < K) *reinterpret_cast<uint2*>(xq + (b * L + l) * K + c) = quotients8(sc, v[i]);
+        if (l < L && c < K) *reinterpret_cast<uint2*>(xq + (b * L + l) * K + c) = quotients8(sc, v);
         if (lane == 0) s_scale[g + 16 * i] = sc.s;
     }
     __syncthreads();
@@ -191,7 +210,9 @@ k_quant_weight(const T* __restrict__ w, uint8_t* __restrict__ wq, float* __restr
     for (int i = 0; i < 8; ++i) {
         const int64_t n = nb * kBlk + g + 16 * i;
         if (n < N && c < K) {
-            load8(w + n * K + c, v[i]);
+            Octet<T> o;
+            o.load(w + n * K + c);
+            o.get(v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;

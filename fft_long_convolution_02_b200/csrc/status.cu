@@ -28,8 +28,9 @@ namespace {
 
 static __device__ uint32_t g_kernel_status;
 
-constexpr int kMaxDevices = 64;
+using hyena::kMaxDevices;
 std::mutex g_mutex;
+std::atomic<int> g_sms[kMaxDevices];
 uint32_t* g_word[kMaxDevices] = {};
 
 }  // namespace
@@ -51,6 +52,20 @@ cudaError_t kernel_status_word(uint32_t** out) {
         g_word[dev] = static_cast<uint32_t*>(p);
     }
     *out = g_word[dev];
+    return cudaSuccess;
+}
+
+cudaError_t device_sms(int* dev, int* sms) {
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (*dev < 0 || *dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    int n = g_sms[*dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (e != cudaSuccess) return e;
+        g_sms[*dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
     return cudaSuccess;
 }
 
