@@ -27,6 +27,7 @@
 
 #include <algorithm>
 
+#include "common.cuh"
 #include "delta.h"
 #include "kernels.h"
 #include "tc_util.cuh"
@@ -163,6 +164,13 @@ __device__ __forceinline__ uint4 whole_octet(const bf16* p, const DeltaView& s, 
     return c < nc && t < nt ? __ldg(reinterpret_cast<const uint4*>(p + int64_t(c) * s.sc + int64_t(t) * s.st)) : make_uint4(0, 0, 0, 0);
 }
 
+// The same as an asynchronous copy into shared memory.
+template <bool FIRST>
+__device__ __forceinline__ void copy_octet(void* to, const bf16* p, const DeltaView& s, int c, int t, int nc, int nt) {
+    if (c < nc && t < nt) cp_async_bytes16(to, p + int64_t(c) * s.sc + int64_t(t) * s.st);
+    else *static_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+}
+
 struct ChunkArgs {
     DeltaArgs a;
     uint8_t* blobs;                                // [B][Hv][chunks][kBlob]
@@ -180,24 +188,70 @@ __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
 // ----------------------------------------------------------------------- prep
 // One CTA of four warps a chunk and value head.  K and Q as they are (bf16,
 // products exact in fp32) through mma.sync, warp w the 16 rows from 16 w, only
-// tiles on or under the diagonal.  The inverse of the unit triangle 1 + A in
-// fp32: the two 32 x 32 blocks on the diagonal by substitution (a thread a
-// column, the columns in registers), the block under them as -T22 (A21 T11).
+// tiles on or under the diagonal; the norms are the diagonals of K K^T and Q Q^T.
+// The inverse of the unit triangle 1 + A in fp32: the four 16 x 16 blocks on the
+// diagonal by substitution (a thread a column, the columns in registers), then
+// twice the block under two inverses as -T22 (A21 T11).  Its chain of short
+// steps bounds it, so what counts is how many CTAs an SM holds: A and T lie
+// where K and Q were.
 constexpr int kPrepThreads = 128;
 constexpr int kARow = 68;
 
 template <int DK, bool FIRST>
 struct PrepSmem {
     static constexpr int kRows = FIRST ? DK : C, kPieces = FIRST ? 8 : DK / 8;
-    alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
-    alignas(16) float A[C][kARow], T[C][kARow];
-    float W[32][36];
-    float gh[C], gl[C], rk[C], rq[C], beta[C];
-    float part[2][4][C];
+    union {
+        struct {
+            alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
+        };
+        struct {
+            alignas(16) float A[C][kARow], T[C][kARow];
+        };
+    };
+    alignas(16) float W[32][36];
+    alignas(16) float gh[C], gl[C], rk[C], rq[C], beta[C];         // gh + gl: sums of the log2 decays
 };
 
+// W = A[r0 + N ..][c0 ..] T[c0 ..][c0 ..], then T[r0 ..][c0 ..] = -T[r0 ..][r0 ..] W, for the N x N block under the
+// diagonal block at c0 (r0 = c0 + N), by `threads` threads of four columns each.
+template <int N, typename Sm>
+__device__ __forceinline__ void block_under(Sm& sm, int c0, int wrow, int t) {
+    constexpr int kGroups = N / 4;
+    const int r = t / kGroups, c = (t % kGroups) * 4, r0 = c0 + N;
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+        constexpr int kRowsEach = N * kGroups / (N == 32 ? 128 : 64);          // rows a thread
+        float acc[kRowsEach][4];
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < N; ++k) {
+            const float4 u = step == 0 ? *reinterpret_cast<const float4*>(&sm.T[c0 + k][c0 + c])
+                                       : *reinterpret_cast<const float4*>(&sm.W[wrow + k][c]);
+#pragma unroll
+            for (int i = 0; i < kRowsEach; ++i) {
+                const int row = r + i * (N / kRowsEach);
+                const float w = step == 0 ? sm.A[r0 + row][c0 + k] : -sm.T[r0 + row][r0 + k];
+                acc[i][0] = fmaf(w, u.x, acc[i][0]);
+                acc[i][1] = fmaf(w, u.y, acc[i][1]);
+                acc[i][2] = fmaf(w, u.z, acc[i][2]);
+                acc[i][3] = fmaf(w, u.w, acc[i][3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsEach; ++i) {
+            const int row = r + i * (N / kRowsEach);
+            float* to = step == 0 ? &sm.W[wrow + row][c] : &sm.T[r0 + row][c0 + c];
+            *reinterpret_cast<float4*>(to) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        }
+        __syncthreads();
+    }
+}
+
 template <int DK, bool FIRST>
-__global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
+__global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
     using Sm = PrepSmem<DK, FIRST>;
     constexpr int P = Sm::kPieces;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -214,18 +268,11 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
     const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc + t0 * a.qs.st;
     constexpr int kOct = Sm::kRows * P / kPrepThreads;
     if (whole<FIRST>(a.dk, n, x.vec_k && x.vec_q)) {
-        uint4 w[2][kOct];
 #pragma unroll
         for (int j = 0; j < kOct; ++j) {
             const int row = (tid + j * kPrepThreads) / P, c = (tid + j * kPrepThreads) % P;
-            w[0][j] = whole_octet<FIRST>(kp, a.ks, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
-            w[1][j] = whole_octet<FIRST>(qp, a.qs, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
-        }
-#pragma unroll
-        for (int j = 0; j < kOct; ++j) {
-            const int row = (tid + j * kPrepThreads) / P, c = (tid + j * kPrepThreads) % P;
-            *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = w[0][j];
-            *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = w[1][j];
+            copy_octet<FIRST>(sm.k + piece<P>(row, c), kp, a.ks, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
+            copy_octet<FIRST>(sm.q + piece<P>(row, c), qp, a.qs, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
         }
     } else {
 #pragma unroll 1
@@ -236,15 +283,17 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
             *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n, x.vec_q);
         }
     }
-    // sums of the log decays as two floats (in double here), by the first warp: two tokens a lane
+    cp_async_commit();
+    // sums of the log2 decays as two floats (in double here), by the first warp: two tokens a lane
     if (warp == 0) {
         double v[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int t = 2 * lane + j;
-            // -inf (empty the state) as a finite decay that underflows to 0 against everything
-            v[j] = (a.g && t < n) ? double(fmaxf(a.g[b * a.gs.sb + h * a.gs.sc + (t0 + t) * a.gs.st], -1e5f)) : 0.0;
-            if (a.g && t < n && isnan(a.g[b * a.gs.sb + h * a.gs.sc + (t0 + t) * a.gs.st])) v[j] = __longlong_as_double(0x7ff8000000000000ll);
+            float d = a.g && t < n ? a.g[b * a.gs.sb + h * a.gs.sc + (t0 + t) * a.gs.st] : 0.0f;
+            // -inf (empty the state) as a finite decay that underflows to 0 against everything; NaN stays
+            d = d < -1e5f ? -1e5f : d;
+            v[j] = double(d) * 1.4426950408889634;
             sm.beta[t] = t < n ? (a.beta ? a.beta[b * a.bs.sb + h * a.bs.sc + (t0 + t) * a.bs.st] : 1.0f) : 0.0f;
         }
         double s = v[0] + v[1];
@@ -259,83 +308,32 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
         sm.gh[2 * lane + 1] = float(s);
         sm.gl[2 * lane + 1] = float(s - double(float(s)));
     }
+    cp_async_wait_all();
     __syncthreads();
-    // norms and largest elements of the rows: two threads a token, half of the channels each
-    {
-        const int t = tid & (C - 1), half = tid >> 6;
-        float k2 = 0.0f, q2 = 0.0f, km = 0.0f, qm = 0.0f;
-        if constexpr (FIRST) {
-#pragma unroll 8
-            for (int c = half * (DK / 2); c < (half + 1) * (DK / 2); ++c) {
-                const uint32_t at = piece<P>(c, t >> 3) + uint32_t(t & 7) * 2u;
-                const float kv = __bfloat162float(*reinterpret_cast<const bf16*>(sm.k + at));
-                const float qv = __bfloat162float(*reinterpret_cast<const bf16*>(sm.q + at));
-                k2 = fmaf(kv, kv, k2);
-                q2 = fmaf(qv, qv, q2);
-                km = fmaxf(km, fabsf(kv));
-                qm = fmaxf(qm, fabsf(qv));
-            }
-        } else {
-#pragma unroll
-            for (int c = half * (P / 2); c < (half + 1) * (P / 2); ++c) {
-                const uint4 kw = *reinterpret_cast<const uint4*>(sm.k + piece<P>(t, c));
-                const uint4 qw = *reinterpret_cast<const uint4*>(sm.q + piece<P>(t, c));
-                const uint32_t ku[4] = {kw.x, kw.y, kw.z, kw.w}, qu[4] = {qw.x, qw.y, qw.z, qw.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float kv = bf(ku[i >> 1], i & 1), qv = bf(qu[i >> 1], i & 1);
-                    k2 = fmaf(kv, kv, k2);
-                    q2 = fmaf(qv, qv, q2);
-                    km = fmaxf(km, fabsf(kv));
-                    qm = fmaxf(qm, fabsf(qv));
-                }
-            }
-        }
-        sm.part[half][0][t] = k2;
-        sm.part[half][1][t] = q2;
-        sm.part[half][2][t] = km;
-        sm.part[half][3][t] = qm;
-    }
-    __syncthreads();
-    uint8_t* blob = x.blobs + ((b * a.Hv + h) * int64_t(x.chunks) + chunk) * kBlob;
-    Factors* f = reinterpret_cast<Factors*>(blob + 3 * kTile);
-    if (tid < C) {
-        const int t = tid;
-        const float rk = a.l2norm ? 1.0f / sqrtf(sm.part[0][0][t] + sm.part[1][0][t] + kDeltaNormEps) : 1.0f;
-        const float rq = (a.l2norm ? 1.0f / sqrtf(sm.part[0][1][t] + sm.part[1][1][t] + kDeltaNormEps) : 1.0f) * a.scale;
-        sm.rk[t] = rk;
-        sm.rq[t] = rq;
-        const Pow2 pk(fmaxf(sm.part[0][2][t], sm.part[1][2][t])), pq(fmaxf(sm.part[0][3][t], sm.part[1][3][t]));
-        const float into = expf(sm.gh[t] + sm.gl[t]);
-        const float out = expf((sm.gh[C - 1] - sm.gh[t]) + (sm.gl[C - 1] - sm.gl[t]));
-        f->kmul[t] = pk.up;
-        f->qmul[t] = pq.up;
-        f->cx[t] = into * rk * pk.down;
-        f->cu[t] = out * rk * pk.down;
-        f->co[t] = into * rq * pq.down;
-        if (t == 0) f->gamma = expf(sm.gh[C - 1] + sm.gl[C - 1]);
-    }
-    // K K^T and Q K^T, rows 16 warp ..
+    // K K^T and Q K^T, rows 16 warp .., and the diagonal block of Q Q^T
     const uint32_t tk = tc::smem_u32(sm.k), tq = tc::smem_u32(sm.q);
-    float ka[8][4], qa[8][4];
+    float ka[8][4], qa[8][4], qq[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ka[i][j] = qa[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) ka[i][j] = qa[i][j] = qq[i & 1][j] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t lk[4], lq[4];
+        uint32_t lk[4], lq[4], r[4];
         if constexpr (FIRST) {
             left_km<P>(lk, tk, warp, ks, lane);
             left_km<P>(lq, tq, warp, ks, lane);
+            right_kn<P>(r, tq, ks, 2 * warp, lane);
         } else {
             left_mk<P>(lk, tk, warp, ks, lane);
             left_mk<P>(lq, tq, warp, ks, lane);
+            right_nk<P>(r, tq, ks, 2 * warp, lane);
         }
+        mma_bf16(qq[0], lq, r[0], r[1]);
+        mma_bf16(qq[1], lq, r[2], r[3]);
 #pragma unroll
         for (int nt = 0; nt < 8; nt += 2) {
             if (nt > 2 * warp) break;
-            uint32_t r[4];
             if constexpr (FIRST) right_kn<P>(r, tk, ks, nt, lane);
             else right_nk<P>(r, tk, ks, nt, lane);
             mma_bf16(ka[nt], lk, r[0], r[1]);
@@ -344,35 +342,66 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
             mma_bf16(qa[nt + 1], lq, r[2], r[3]);
         }
     }
-    __syncthreads();                               // rk, rq
-    float pm[2] = {0.0f, 0.0f};
+    uint8_t* blob = x.blobs + ((b * a.Hv + h) * int64_t(x.chunks) + chunk) * kBlob;
+    Factors* f = reinterpret_cast<Factors*>(blob + 3 * kTile);
+    // row g of the diagonal's two tiles meets its own column in the thread that holds column pair g / 2
+    if (t4 == g >> 1) {
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+        for (int i = 0; i < 2; ++i) {
+            const int t = 16 * warp + g + 8 * i, at = 2 * i + (g & 1);
+            float k2 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 16 * warp + g + 8 * (j >> 1), c = 8 * nt + 2 * t4 + (j & 1);
-            const float d = c <= r ? expf((sm.gh[r] - sm.gh[c]) + (sm.gl[r] - sm.gl[c])) * sm.rk[c] : 0.0f;
-            sm.A[r][c] = c < r ? sm.beta[r] * sm.rk[r] * d * ka[nt][j] : 0.0f;
-            qa[nt][j] = c <= r ? d * sm.rq[r] * qa[nt][j] : 0.0f;
-            pm[j >> 1] = fmaxf(pm[j >> 1], fabsf(qa[nt][j]));
+            for (int w = 0; w < 4; ++w)
+                if (w == warp) k2 = at == 0 ? ka[2 * w][0] : at == 1 ? ka[2 * w][1] : at == 2 ? ka[2 * w + 1][2] : ka[2 * w + 1][3];
+            const float q2 = at == 0 ? qq[0][0] : at == 1 ? qq[0][1] : at == 2 ? qq[1][2] : qq[1][3];
+            const float rk = a.l2norm ? 1.0f / sqrtf(k2 + kDeltaNormEps) : 1.0f;
+            const float rq = (a.l2norm ? 1.0f / sqrtf(q2 + kDeltaNormEps) : 1.0f) * a.scale;
+            sm.rk[t] = rk;
+            sm.rq[t] = rq;
+            // a row's largest element is at most its norm; a norm whose square may have underflowed counts as 1e-18
+            const Pow2 pk(fmaxf(sqrtf(k2), 1e-18f)), pq(fmaxf(sqrtf(q2), 1e-18f));
+            const float into = exp2f(sm.gh[t] + sm.gl[t]);
+            const float out = exp2f((sm.gh[C - 1] - sm.gh[t]) + (sm.gl[C - 1] - sm.gl[t]));
+            f->kmul[t] = pk.up;
+            f->qmul[t] = pq.up;
+            f->cx[t] = into * rk * pk.down;
+            f->cu[t] = out * rk * pk.down;
+            f->co[t] = into * rq * pq.down;
+            if (t == 0) f->gamma = exp2f(sm.gh[C - 1] + sm.gl[C - 1]);
         }
-    const Pow2 p0(quad_max(pm[0])), p1(quad_max(pm[1]));
-    if (t4 == 0) {
-        f->cp[16 * warp + g] = p0.down;
-        f->cp[16 * warp + g + 8] = p1.down;
     }
+    __syncthreads();                               // rk, rq; and K, Q have been read
+    float pm[2] = {0.0f, 0.0f};
+    {
+        const int r0 = 16 * warp + g, r1 = r0 + 8;
+        const float h0 = sm.gh[r0], h1 = sm.gh[r1], l0 = sm.gl[r0], l1 = sm.gl[r1];
+        const float a0 = sm.beta[r0] * sm.rk[r0], a1 = sm.beta[r1] * sm.rk[r1], q0 = sm.rq[r0], q1 = sm.rq[r1];
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        uint8_t* P2 = blob + 2 * kTile + 4 * t4;
-        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g, nt)) = pack_h(qa[nt][0] * p0.up, qa[nt][1] * p0.up);
-        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g + 8, nt)) = pack_h(qa[nt][2] * p1.up, qa[nt][3] * p1.up);
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt > 2 * warp + 1) break;          // what lies right of the diagonal's blocks is not read
+            const int c = 8 * nt + 2 * t4;
+            const float2 hc = *reinterpret_cast<const float2*>(&sm.gh[c]), lc = *reinterpret_cast<const float2*>(&sm.gl[c]);
+            const float2 rc = *reinterpret_cast<const float2*>(&sm.rk[c]);
+            const float d[4] = {exp2f((h0 - hc.x) + (l0 - lc.x)) * rc.x, exp2f((h0 - hc.y) + (l0 - lc.y)) * rc.y,
+                                exp2f((h1 - hc.x) + (l1 - lc.x)) * rc.x, exp2f((h1 - hc.y) + (l1 - lc.y)) * rc.y};
+            float av[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = j < 2 ? r0 : r1, cc = c + (j & 1);
+                av[j] = cc < r ? (j < 2 ? a0 : a1) * d[j] * ka[nt][j] : 0.0f;
+                qa[nt][j] = cc <= r ? d[j] * (j < 2 ? q0 : q1) * qa[nt][j] : 0.0f;
+                pm[j >> 1] = fmaxf(pm[j >> 1], fabsf(qa[nt][j]));
+            }
+            *reinterpret_cast<float2*>(&sm.A[r0][c]) = make_float2(av[0], av[1]);
+            *reinterpret_cast<float2*>(&sm.A[r1][c]) = make_float2(av[2], av[3]);
+        }
     }
     __syncthreads();
-    if (warp < 2) {
-        const int o = 32 * warp;
-        float xx[32];
+    if (lane < 16) {
+        const int o = 16 * warp;
+        float xx[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
             float s0 = i == lane ? 1.0f : 0.0f, s1 = 0.0f;
 #pragma unroll
             for (int j = 0; j < i; j += 4) {
@@ -385,36 +414,27 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
             xx[i] = s0 + s1;
             sm.T[o + i][o + lane] = xx[i];
         }
+    } else if (!(warp & 1)) {
+        // right of the first and third block: read as part of a 32 x 32 inverse
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sm.T[16 * warp + i][16 * warp + lane] = 0.0f;
+    }
+    // P leaves while the substitutions run
+    const Pow2 p0(quad_max(pm[0])), p1(quad_max(pm[1]));
+    if (t4 == 0) {
+        f->cp[16 * warp + g] = p0.down;
+        f->cp[16 * warp + g + 8] = p1.down;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt > 2 * warp + 1) break;
+        uint8_t* P2 = blob + 2 * kTile + 4 * t4;
+        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g, nt)) = pack_h(qa[nt][0] * p0.up, qa[nt][1] * p0.up);
+        *reinterpret_cast<uint32_t*>(P2 + piece<8>(16 * warp + g + 8, nt)) = pack_h(qa[nt][2] * p1.up, qa[nt][3] * p1.up);
     }
     __syncthreads();
-    {
-        const int r = tid >> 2, c = (tid & 3) * 8;
-        float acc[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float w = sm.A[32 + r][k];
-            const float4 u = *reinterpret_cast<const float4*>(&sm.T[k][c]), v = *reinterpret_cast<const float4*>(&sm.T[k][c + 4]);
-            acc[0] = fmaf(w, u.x, acc[0]); acc[1] = fmaf(w, u.y, acc[1]); acc[2] = fmaf(w, u.z, acc[2]); acc[3] = fmaf(w, u.w, acc[3]);
-            acc[4] = fmaf(w, v.x, acc[4]); acc[5] = fmaf(w, v.y, acc[5]); acc[6] = fmaf(w, v.z, acc[6]); acc[7] = fmaf(w, v.w, acc[7]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sm.W[r][c + i] = acc[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float w = -sm.T[32 + r][32 + k];
-            const float4 u = *reinterpret_cast<const float4*>(&sm.W[k][c]), v = *reinterpret_cast<const float4*>(&sm.W[k][c + 4]);
-            acc[0] = fmaf(w, u.x, acc[0]); acc[1] = fmaf(w, u.y, acc[1]); acc[2] = fmaf(w, u.z, acc[2]); acc[3] = fmaf(w, u.w, acc[3]);
-            acc[4] = fmaf(w, v.x, acc[4]); acc[5] = fmaf(w, v.y, acc[5]); acc[6] = fmaf(w, v.z, acc[6]); acc[7] = fmaf(w, v.w, acc[7]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sm.T[32 + r][c + i] = acc[i];
-    }
-    __syncthreads();
+    block_under<16>(sm, 32 * (tid >> 6), 16 * (tid >> 6), tid & 63);
+    block_under<32>(sm, 0, 0, tid);
     // T diag(beta) in two parts: two threads a row, half of the columns each
     {
         const int r = tid >> 1, c0 = (tid & 1) * 32;
@@ -430,6 +450,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(ChunkArgs x) {
         if (c0 == 0) f->ct[r] = p.down;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            if (c0 + 8 * i > (r | 15)) break;
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split_h(v[8 * i + 2 * j] * p.up, v[8 * i + 2 * j + 1] * p.up, hi[j], lo[j]);
@@ -473,34 +494,36 @@ __device__ __forceinline__ uint4 scaled8(const uint4& w, const float (&m)[8]) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// A K or Q tile to fp16 under the tokens' powers of two: m holds those of this thread's eight tokens (FIRST), mul
-// those of all.
+// A K or Q tile into shared memory, then (by the same threads, each its own octets) to fp16 in place under the tokens'
+// powers of two: m holds those of this thread's eight tokens (FIRST), mul those of all.
 template <int DK, bool FIRST>
-__device__ __forceinline__ void load_scaled(uint8_t* tile, const bf16* p, const DeltaView& s, const float (&m)[8],
-                                            const float* mul, int dk, int n, bool vec, int lt) {
+__device__ __forceinline__ void load_tile(uint8_t* tile, const bf16* p, const DeltaView& s, int dk, int n, bool vec, int lt) {
     constexpr int P = FIRST ? 8 : DK / 8, kOct = C * DK / 8 / kLoaders;
-    auto put = [&](int i, const uint4& w) {
-        const int row = i / P, c = i % P;
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = FIRST ? m[j] : mul[row];
-        *reinterpret_cast<uint4*>(tile + piece<P>(row, c)) = scaled8(w, f);
-    };
     if (whole<FIRST>(dk, n, vec)) {
-        uint4 w[kOct];
 #pragma unroll
         for (int j = 0; j < kOct; ++j) {
             const int row = (lt + j * kLoaders) / P, c = (lt + j * kLoaders) % P;
-            w[j] = whole_octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n);
+            copy_octet<FIRST>(tile + piece<P>(row, c), p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n);
         }
-#pragma unroll
-        for (int j = 0; j < kOct; ++j) put(lt + j * kLoaders, w[j]);
     } else {
 #pragma unroll 1
         for (int i = lt; i < C * DK / 8; i += kLoaders) {
             const int row = i / P, c = i % P;
-            put(i, octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n, vec));
+            *reinterpret_cast<uint4*>(tile + piece<P>(row, c)) = octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n, vec);
         }
+    }
+}
+template <int DK, bool FIRST>
+__device__ __forceinline__ void scale_tile(uint8_t* tile, const float (&m)[8], const float* mul, int lt) {
+    constexpr int P = FIRST ? 8 : DK / 8, kOct = C * DK / 8 / kLoaders;
+#pragma unroll
+    for (int j = 0; j < kOct; ++j) {
+        const int row = (lt + j * kLoaders) / P, c = (lt + j * kLoaders) % P;
+        uint4* at = reinterpret_cast<uint4*>(tile + piece<P>(row, c));
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = FIRST ? m[i] : mul[row];
+        *at = scaled8(*at, f);
     }
 }
 
@@ -512,11 +535,11 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
     if constexpr (FIRST) {
         auto put = [&](int i, const uint4& w) { *reinterpret_cast<uint4*>(&v[i / 8][8 * (i % 8)]) = w; };
         if (whole<true>(cols, n, vec)) {
-            uint4 w[kOct];
 #pragma unroll
-            for (int j = 0; j < kOct; ++j) w[j] = whole_octet<true>(p, s, (lt + j * kLoaders) / 8, 8 * ((lt + j * kLoaders) % 8), cols, n);
-#pragma unroll
-            for (int j = 0; j < kOct; ++j) put(lt + j * kLoaders, w[j]);
+            for (int j = 0; j < kOct; ++j) {
+                const int i = lt + j * kLoaders;
+                copy_octet<true>(&v[i / 8][8 * (i % 8)], p, s, i / 8, 8 * (i % 8), cols, n);
+            }
         } else {
 #pragma unroll 1
             for (int i = lt; i < 16 * NW * 8; i += kLoaders) put(i, octet<true>(p, s, i / 8, 8 * (i % 8), cols, n, vec));
@@ -596,6 +619,8 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             }
             const int64_t t0 = int64_t(ch) * C;
             const int n = int(min(int64_t(C), len - t0));
+            load_tile<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, a.dk, n, x.vec_k, lt);
+            load_tile<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, a.dk, n, x.vec_q, lt);
             const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
             float mk[8], mq[8];
             if constexpr (FIRST) {
@@ -605,9 +630,11 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
                     mq[i] = f->qmul[8 * (lt % 8) + i];
                 }
             }
-            load_scaled<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, mk, f->kmul, a.dk, n, x.vec_k, lt);
-            load_scaled<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, mq, f->qmul, a.dk, n, x.vec_q, lt);
             load_values<NW, FIRST>(st.v, vp + t0 * a.vs.st, a.vs, cols, n, x.vec_v, lt);
+            cp_async_commit();
+            cp_async_wait_all();
+            scale_tile<DK, FIRST>(st.k, mk, f->kmul, lt);
+            scale_tile<DK, FIRST>(st.q, mq, f->qmul, lt);
             tc::mbar_arrive(&sm.full[s]);
         }
         // the last copies have landed before the CTA may end: the scanning warps wait for every stage
