@@ -65,12 +65,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
 // registers here, and a CTA's 16 x 64 operands are below tcgen05's 128 rows.
 constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
+constexpr int kORow = 16;                          // elements of a token's row of a warp's outputs
 
 template <int DK, int NW>
 struct ScanSmem {
@@ -482,7 +483,7 @@ struct ScanSmem {
         alignas(128) uint8_t blob[kBlob];          // T high, T low, P, factors
         alignas(16) bf16 v[16 * NW][kVRow];
     } st[2];
-    alignas(16) bf16 o[NW][16 * kVRow];            // [channel][time], or [time][16 + 8]
+    alignas(16) bf16 o[NW][16 * kVRow];            // [channel][kVRow], or [time][kORow]
     uint64_t full[2], empty[2];
 };
 
@@ -678,30 +679,36 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) X[i][j] = O[i][j] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                split_h(S[2 * ks + j][0] * ps0.up, S[2 * ks + j][1] * ps0.up, hi[2 * j], lo[2 * j]);
-                split_h(S[2 * ks + j][2] * ps1.up, S[2 * ks + j][3] * ps1.up, hi[2 * j + 1], lo[2 * j + 1]);
+        // right operands are read a step (six products) ahead of their use
+        auto keys = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+            if constexpr (FIRST) {
+                right_kn<P>(r, tk, step / 4, 2 * (step % 4), lane);
+                right_kn<P>(w, tq, step / 4, 2 * (step % 4), lane);
+            } else {
+                right_nk<P>(r, tk, step / 4, 2 * (step % 4), lane);
+                right_nk<P>(w, tq, step / 4, 2 * (step % 4), lane);
             }
+        };
+        {
+            uint32_t r[2][4], w[2][4], hi[4], lo[4];
+            keys(r[0], w[0], 0);
 #pragma unroll
-            for (int nt = 0; nt < 8; nt += 2) {
-                uint32_t r[4], w[4];
-                if constexpr (FIRST) {
-                    right_kn<P>(r, tk, ks, nt, lane);
-                    right_kn<P>(w, tq, ks, nt, lane);
-                } else {
-                    right_nk<P>(r, tk, ks, nt, lane);
-                    right_nk<P>(w, tq, ks, nt, lane);
+            for (int step = 0; step < DK / 4; ++step) {
+                const int ks = step / 4, nt = 2 * (step % 4), at = step & 1;
+                if (step + 1 < DK / 4) keys(r[at ^ 1], w[at ^ 1], step + 1);
+                if (nt == 0) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        split_h(S[2 * ks + j][0] * ps0.up, S[2 * ks + j][1] * ps0.up, hi[2 * j], lo[2 * j]);
+                        split_h(S[2 * ks + j][2] * ps1.up, S[2 * ks + j][3] * ps1.up, hi[2 * j + 1], lo[2 * j + 1]);
+                    }
                 }
-                mma_f16(X[nt], hi, r[0], r[1]);
-                mma_f16(X[nt + 1], hi, r[2], r[3]);
-                mma_f16(O[nt], hi, w[0], w[1]);
-                mma_f16(O[nt + 1], hi, w[2], w[3]);
-                mma_f16(X[nt], lo, r[0], r[1]);
-                mma_f16(X[nt + 1], lo, r[2], r[3]);
+                mma_f16(X[nt], hi, r[at][0], r[at][1]);
+                mma_f16(X[nt + 1], hi, r[at][2], r[at][3]);
+                mma_f16(O[nt], hi, w[at][0], w[at][1]);
+                mma_f16(O[nt + 1], hi, w[at][2], w[at][3]);
+                mma_f16(X[nt], lo, r[at][0], r[at][1]);
+                mma_f16(X[nt + 1], lo, r[at][2], r[at][3]);
             }
         }
         // R^T = V^T - X^T diag(cx); the outputs' part of the state
@@ -781,38 +788,47 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
                 split_h(X[2 * ks + j][2] * pw1.up, X[2 * ks + j][3] * pw1.up, hi[ks][2 * j + 1], lo[ks][2 * j + 1]);
             }
         const float gamma = f.gamma;
-#pragma unroll
-        for (int nt = 0; nt < DK / 8; nt += 4) {
+        auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+            const int ks = step % 4, nt = 4 * (step / 4);
+            if constexpr (FIRST) {
+                right_nk<P>(r, tk, ks, nt, lane);
+                right_nk<P>(w, tk, ks, nt + 2, lane);
+            } else {
+                right_kn<P>(r, tk, ks, nt, lane);
+                right_kn<P>(w, tk, ks, nt + 2, lane);
+            }
+        };
+        {
+            uint32_t r[2][4], w[2][4];
+            keys_t(r[0], w[0], 0);
             float D[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int step = 0; step < DK / 8; ++step) {
+                const int ks = step % 4, nt = 4 * (step / 4), at = step & 1;
+                if (step + 1 < DK / 8) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
+                if (ks == 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) D[i][j] = 0.0f;
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                uint32_t r[4], w[4];
-                if constexpr (FIRST) {
-                    right_nk<P>(r, tk, ks, nt, lane);
-                    right_nk<P>(w, tk, ks, nt + 2, lane);
-                } else {
-                    right_kn<P>(r, tk, ks, nt, lane);
-                    right_kn<P>(w, tk, ks, nt + 2, lane);
+                        for (int j = 0; j < 4; ++j) D[i][j] = 0.0f;
                 }
-                mma_f16(D[0], hi[ks], r[0], r[1]);
-                mma_f16(D[1], hi[ks], r[2], r[3]);
-                mma_f16(D[2], hi[ks], w[0], w[1]);
-                mma_f16(D[3], hi[ks], w[2], w[3]);
-                mma_f16(D[0], lo[ks], r[0], r[1]);
-                mma_f16(D[1], lo[ks], r[2], r[3]);
-                mma_f16(D[2], lo[ks], w[0], w[1]);
-                mma_f16(D[3], lo[ks], w[2], w[3]);
-            }
+                mma_f16(D[0], hi[ks], r[at][0], r[at][1]);
+                mma_f16(D[1], hi[ks], r[at][2], r[at][3]);
+                mma_f16(D[2], hi[ks], w[at][0], w[at][1]);
+                mma_f16(D[3], hi[ks], w[at][2], w[at][3]);
+                mma_f16(D[0], lo[ks], r[at][0], r[at][1]);
+                mma_f16(D[1], lo[ks], r[at][2], r[at][3]);
+                mma_f16(D[2], lo[ks], w[at][0], w[at][1]);
+                mma_f16(D[3], lo[ks], w[at][2], w[at][3]);
+                if (ks == 3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                S[nt + i][0] = fmaf(gamma, S[nt + i][0], D[i][0] * pw0.down);
-                S[nt + i][1] = fmaf(gamma, S[nt + i][1], D[i][1] * pw0.down);
-                S[nt + i][2] = fmaf(gamma, S[nt + i][2], D[i][2] * pw1.down);
-                S[nt + i][3] = fmaf(gamma, S[nt + i][3], D[i][3] * pw1.down);
+                    for (int i = 0; i < 4; ++i) {
+                        S[nt + i][0] = fmaf(gamma, S[nt + i][0], D[i][0] * pw0.down);
+                        S[nt + i][1] = fmaf(gamma, S[nt + i][1], D[i][1] * pw0.down);
+                        S[nt + i][2] = fmaf(gamma, S[nt + i][2], D[i][2] * pw1.down);
+                        S[nt + i][3] = fmaf(gamma, S[nt + i][3], D[i][3] * pw1.down);
+                    }
+                }
             }
         }
         // O^T += U^T P^T
@@ -847,10 +863,10 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
                 *reinterpret_cast<__nv_bfloat162*>(so + g * kVRow + t) = y0;
                 *reinterpret_cast<__nv_bfloat162*>(so + (g + 8) * kVRow + t) = y1;
             } else {
-                so[t * 16 + g] = y0.x;
-                so[(t + 1) * 16 + g] = y0.y;
-                so[t * 16 + g + 8] = y1.x;
-                so[(t + 1) * 16 + g + 8] = y1.y;
+                so[t * kORow + g] = y0.x;
+                so[(t + 1) * kORow + g] = y0.y;
+                so[t * kORow + g + 8] = y1.x;
+                so[(t + 1) * kORow + g + 8] = y1.y;
             }
         }
         __syncwarp();
@@ -858,8 +874,26 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         const int64_t t0 = int64_t(ch) * C;
         const int n = int(min(int64_t(C), len - t0)), cols = min(16, a.dv - dw);
         bf16* oc = ob + t0 * a.os.st;
-        if constexpr (FIRST) {
+        if (x.vec_o && n == C && cols == 16) {
+            // whole rows of 16 bytes, all in flight
+            uint4 w[4];
+            if constexpr (FIRST) {
+                const int r = lane >> 3, t = (lane & 7) * 8;
 #pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(so + (r + 4 * j) * kVRow + t);
+                bf16* to = oc + int64_t(r) * a.os.sc + t;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(to + 4 * j * a.os.sc) = w[j];
+            } else {
+                const int t = lane >> 1, c = (lane & 1) * 8;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(so + (t + 16 * j) * kORow + c);
+                bf16* to = oc + int64_t(t) * a.os.st + c;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(to + 16 * j * a.os.st) = w[j];
+            }
+        } else if constexpr (FIRST) {
+#pragma unroll 1
             for (int i = lane; i < 16 * 8; i += 32) {
                 const int r = i >> 3, t = (i & 7) * 8;
                 if (r >= cols) continue;
@@ -870,14 +904,14 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
                 }
             }
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int i = lane; i < C * 2; i += 32) {
                 const int t = i >> 1, c = (i & 1) * 8;
                 if (t >= n) continue;
                 if (x.vec_o && c + 8 <= cols) {
-                    *reinterpret_cast<uint4*>(oc + int64_t(t) * a.os.st + c) = *reinterpret_cast<const uint4*>(so + t * 16 + c);
+                    *reinterpret_cast<uint4*>(oc + int64_t(t) * a.os.st + c) = *reinterpret_cast<const uint4*>(so + t * kORow + c);
                 } else {
-                    for (int j = 0; j < 8 && c + j < cols; ++j) oc[int64_t(t) * a.os.st + int64_t(c + j) * a.os.sc] = so[t * 16 + c + j];
+                    for (int j = 0; j < 8 && c + j < cols; ++j) oc[int64_t(t) * a.os.st + int64_t(c + j) * a.os.sc] = so[t * kORow + c + j];
                 }
             }
         }
