@@ -176,19 +176,22 @@ cudaError_t launch_seq_t(const DeltaArgs& a, cudaStream_t s) {
 
 // ----------------------------------------------------------------------- step
 // One token.  The state is read and written once, so its traffic bounds the
-// kernel: 256 threads hold dk x 32 columns in registers (V columns a thread as
-// one load of 4 V bytes, rows rg + R j), all loads issued before the first
-// barrier, one reduction over the rows for both contractions.  V = 4 needs dv a
-// multiple of 4 (the rows of the state 16-byte aligned).
-constexpr int kStepThreads = 256, kStepCols = 32;
+// kernel: 256 threads hold dk x kStepCols columns in registers (V columns a
+// thread as one load of 4 V bytes, rows rg + R j), all loads issued before the
+// first barrier, one reduction over the rows for both contractions.  V = 4
+// needs dv a multiple of 4 (the rows of the state 16-byte aligned).  With many
+// states a CTA takes 128 columns, 64 KB in flight; with few 32, which reach more
+// SMs.
+constexpr int kStepThreads = 256;
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kStepThreads, 5)
+template <typename T, int V, int kStepCols>
+__global__ void __launch_bounds__(kStepThreads)
 k_delta_step(DeltaArgs a, float* __restrict__ states, int64_t n_states, const int32_t* __restrict__ slots,
              uint32_t* status) {
     constexpr int CG = kStepCols / V;              // threads along a row of 32 columns
     constexpr int R = kStepThreads / CG;           // row groups
     constexpr int J = kDeltaMaxDk / R;             // rows a thread
+    static_assert(CG <= 32, "a row group is within a warp");
     __shared__ float sk[kDeltaMaxDk], sq[kDeltaMaxDk];
     __shared__ float red[kStepThreads / 32][2][kStepCols];
     __shared__ float s_qk;
@@ -433,14 +436,23 @@ cudaError_t launch_delta_seq(const DeltaArgs& a, int dtype, cudaStream_t s) {
 
 cudaError_t launch_delta_step(const DeltaArgs& a, int dtype, float* states, int64_t n_states, const int32_t* slots,
                               uint32_t* status, cudaStream_t s) {
-    const dim3 grid(unsigned((a.dv + kStepCols - 1) / kStepCols), unsigned(a.Hv), unsigned(a.B));
-    const bool v4 = a.dv % 4 == 0;
+    int dev = 0, sms = 0;
+    const cudaError_t e = device_sms(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    // 128 columns a CTA once that leaves every SM two (256 rows of 16 heads, dk = dv = 128: 108 us against 152 us with 32); rows of 4 columns
+    // as one access where they are aligned
+    const bool v4 = a.dv % 4 == 0, wide = v4 && a.dv > 64 && a.B * a.Hv >= 2 * int64_t(sms);
+    const int cols = wide ? 128 : 32;
+    const dim3 grid(unsigned((a.dv + cols - 1) / cols), unsigned(a.Hv), unsigned(a.B));
+    auto go = [&](auto kernel) { kernel<<<grid, kStepThreads, 0, s>>>(a, states, n_states, slots, status); };
     if (dtype == DT_BF16) {
-        if (v4) k_delta_step<__nv_bfloat16, 4><<<grid, kStepThreads, 0, s>>>(a, states, n_states, slots, status);
-        else k_delta_step<__nv_bfloat16, 1><<<grid, kStepThreads, 0, s>>>(a, states, n_states, slots, status);
+        if (wide) go(k_delta_step<__nv_bfloat16, 4, 128>);
+        else if (v4) go(k_delta_step<__nv_bfloat16, 4, 32>);
+        else go(k_delta_step<__nv_bfloat16, 1, 32>);
     } else {
-        if (v4) k_delta_step<float, 4><<<grid, kStepThreads, 0, s>>>(a, states, n_states, slots, status);
-        else k_delta_step<float, 1><<<grid, kStepThreads, 0, s>>>(a, states, n_states, slots, status);
+        if (wide) go(k_delta_step<float, 4, 128>);
+        else if (v4) go(k_delta_step<float, 4, 32>);
+        else go(k_delta_step<float, 1, 32>);
     }
     return cudaGetLastError();
 }

@@ -476,13 +476,16 @@ constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
 constexpr int kORow = 16;                          // elements of a token's row of a warp's outputs
 
+template <int DK, int VR, int VC>
+struct ScanStage {
+    alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
+    alignas(128) uint8_t blob[kBlob];              // T high, T low, P, factors
+    alignas(16) bf16 v[VR][VC];
+};
 template <int DK, int NW>
 struct ScanSmem {
-    struct Stage {
-        alignas(128) uint8_t k[C * DK * 2], q[C * DK * 2];
-        alignas(128) uint8_t blob[kBlob];          // T high, T low, P, factors
-        alignas(16) bf16 v[16 * NW][kVRow];
-    } st[2];
+    using Stage = ScanStage<DK, 16 * NW, kVRow>;
+    Stage st[2];
     alignas(16) bf16 o[NW][16 * kVRow];            // [channel][kVRow], or [time][kORow]
     uint64_t full[2], empty[2];
 };
@@ -574,6 +577,54 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
     }
 }
 
+// The loading warps of a scanning CTA whose channels start at d0 (cols of them): `put_v` brings V.
+template <int DK, bool FIRST, typename Sm, typename PutV>
+__device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, int lane, int h, int64_t b, int64_t len, int d0,
+                                            PutV put_v) {
+    const DeltaArgs& a = x.a;
+    const int chunks = int((len + C - 1) / C);
+    const int kh = h / (a.Hv / a.Hk);
+    const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc;
+    const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc;
+    const bf16* vp = static_cast<const bf16*>(a.v) + b * a.vs.sb + (int64_t(h) * a.dv + d0) * a.vs.sc;
+    const uint8_t* blobs = x.blobs + (b * a.Hv + h) * int64_t(x.chunks) * kBlob;
+    for (int ch = 0; ch < chunks; ++ch) {
+        const int s = ch & 1;
+        auto& st = sm.st[s];
+        if (!tc::mbar_wait(&sm.empty[s], (uint32_t(ch >> 1) & 1u) ^ 1u, x.budget_ns)) {
+            if (lane == 0) report_status(x.status, kStatusTimeout);
+            break;
+        }
+        const uint8_t* blob = blobs + int64_t(ch) * kBlob;
+        if (lt == 0) {
+            tc::mbar_expect_tx(&sm.full[s], kBlob);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                             tc::smem_u32(st.blob)), "l"(blob), "r"(kBlob), "r"(tc::smem_u32(&sm.full[s]))
+                         : "memory");
+        }
+        const int64_t t0 = int64_t(ch) * C;
+        const int n = int(min(int64_t(C), len - t0));
+        load_tile<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, a.dk, n, x.vec_k, lt);
+        load_tile<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, a.dk, n, x.vec_q, lt);
+        const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
+        float mk[8], mq[8];
+        if constexpr (FIRST) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {          // this thread's eight tokens
+                mk[i] = f->kmul[8 * (lt % 8) + i];
+                mq[i] = f->qmul[8 * (lt % 8) + i];
+            }
+        }
+        put_v(st, vp + t0 * a.vs.st, n);
+        cp_async_commit();
+        cp_async_wait_all();
+        scale_tile<DK, FIRST>(st.k, mk, f->kmul, lt);
+        scale_tile<DK, FIRST>(st.q, mq, f->qmul, lt);
+        tc::mbar_arrive(&sm.full[s]);
+    }
+    // the last copies land before the CTA may end: the scanning warps wait for every stage
+}
+
 template <int DK, int NW, bool FIRST>
 __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs x) {
     using Sm = ScanSmem<DK, NW>;
@@ -597,48 +648,10 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         // ------------------------------------------------------------ loaders
         // registers of eight warps: 384 x 168 at launch = 128 x 56 + 256 x 224
         if constexpr (NW == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-        const int lt = tid - 32 * NW;
-        const int kh = h / (a.Hv / a.Hk);
-        const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc;
-        const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc;
-        const bf16* vp = static_cast<const bf16*>(a.v) + b * a.vs.sb + (int64_t(h) * a.dv + d0) * a.vs.sc;
-        const uint8_t* blobs = x.blobs + (b * a.Hv + h) * int64_t(x.chunks) * kBlob;
-        const int cols = min(16 * NW, a.dv - d0);
-        for (int ch = 0; ch < chunks; ++ch) {
-            const int s = ch & 1;
-            typename Sm::Stage& st = sm.st[s];
-            if (!tc::mbar_wait(&sm.empty[s], (uint32_t(ch >> 1) & 1u) ^ 1u, x.budget_ns)) {
-                if (lane == 0) report_status(x.status, kStatusTimeout);
-                break;
-            }
-            const uint8_t* blob = blobs + int64_t(ch) * kBlob;
-            if (lt == 0) {
-                tc::mbar_expect_tx(&sm.full[s], kBlob);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                                 tc::smem_u32(st.blob)), "l"(blob), "r"(kBlob), "r"(tc::smem_u32(&sm.full[s]))
-                             : "memory");
-            }
-            const int64_t t0 = int64_t(ch) * C;
-            const int n = int(min(int64_t(C), len - t0));
-            load_tile<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, a.dk, n, x.vec_k, lt);
-            load_tile<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, a.dk, n, x.vec_q, lt);
-            const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
-            float mk[8], mq[8];
-            if constexpr (FIRST) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {      // this thread's eight tokens
-                    mk[i] = f->kmul[8 * (lt % 8) + i];
-                    mq[i] = f->qmul[8 * (lt % 8) + i];
-                }
-            }
-            load_values<NW, FIRST>(st.v, vp + t0 * a.vs.st, a.vs, cols, n, x.vec_v, lt);
-            cp_async_commit();
-            cp_async_wait_all();
-            scale_tile<DK, FIRST>(st.k, mk, f->kmul, lt);
-            scale_tile<DK, FIRST>(st.q, mq, f->qmul, lt);
-            tc::mbar_arrive(&sm.full[s]);
-        }
-        // the last copies have landed before the CTA may end: the scanning warps wait for every stage
+        const int lt = tid - 32 * NW, cols = min(16 * NW, a.dv - d0);
+        run_loaders<DK, FIRST>(sm, x, lt, lane, h, b, len, d0, [&](typename Sm::Stage& st, const bf16* p, int n) {
+            load_values<NW, FIRST>(st.v, p, a.vs, cols, n, x.vec_v, lt);
+        });
         return;
     }
     // ------------------------------------------------------------------- scan
@@ -928,6 +941,329 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
     }
 }
 
+// --------------------------------------------------------------- narrow scan
+// For few heads: a warp takes 8 value channels instead of 16, so the same heads
+// make twice the warps and a warp's chain is half as long (1600 cycles of
+// products a chunk).  Time and key channels are the 16 rows of the products,
+// value channels the 8 columns: S [DK x 8] in accumulators,
+//   X = K S,  R = V - diag(cx) X,  U = T R,  S = gamma S + K^T (diag(cu) U),  O = diag(co) Q S + P U,
+// and a result becomes the next one's right operand by transposing its 8 x 8
+// blocks in registers.  Every warp reads all of K, Q, T and P as left operands,
+// so shared memory would bound more than four warps an SM.
+constexpr int kNarrowWarps = 4, kNarrowCols = 8 * kNarrowWarps;
+constexpr int kNarrowVRow = kNarrowCols + 8;       // elements of a token's row of V: eight rows on 32 banks
+
+template <int DK>
+struct NarrowSmem {
+    using Stage = ScanStage<DK, C, kNarrowVRow>;
+    Stage st[2];
+    alignas(16) bf16 o[kNarrowWarps][8 * kVRow];   // [channel][kVRow], or [time][8]
+    uint64_t full[2], empty[2];
+};
+
+// An 8 x 8 block of 16-bit numbers transposed across a warp's registers.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    return r;
+}
+// Two numbers of a 16 x 8 accumulator tile's rows as high and low right operands.
+struct Right {
+    uint32_t hi[2], lo[2];
+    __device__ __forceinline__ Right(const float (&c)[4], float up0, float up1) {
+        uint32_t h0, l0, h1, l1;
+        split_h(c[0] * up0, c[1] * up1, h0, l0);
+        split_h(c[2] * up0, c[3] * up1, h1, l1);
+        hi[0] = transposed(h0);
+        hi[1] = transposed(h1);
+        lo[0] = transposed(l0);
+        lo[1] = transposed(l1);
+    }
+};
+__device__ __forceinline__ float column_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+
+// V [64][kNarrowCols]: as it lies token by token; from channels' rows pairs of channels, eight tokens each way.
+template <bool FIRST>
+__device__ __forceinline__ void load_values_narrow(bf16 (&v)[C][kNarrowVRow], const bf16* p, const DeltaView& s, int cols, int n,
+                                                   bool vec, int lt) {
+    if constexpr (!FIRST) {
+        constexpr int kRowOct = kNarrowCols / 8, kOct = C * kRowOct / kLoaders;
+        if (whole<false>(cols, n, vec)) {
+#pragma unroll
+            for (int j = 0; j < kOct; ++j) {
+                const int i = lt + j * kLoaders;
+                copy_octet<false>(&v[i / kRowOct][8 * (i % kRowOct)], p, s, 8 * (i % kRowOct), i / kRowOct, cols, n);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = lt; i < C * kRowOct; i += kLoaders)
+                *reinterpret_cast<uint4*>(&v[i / kRowOct][8 * (i % kRowOct)]) =
+                    octet<false>(p, s, 8 * (i % kRowOct), i / kRowOct, cols, n, vec);
+        }
+    } else {
+        static_assert(kNarrowCols / 2 * 8 == kLoaders, "a pair of octets a thread");
+        const int cp = lt / 8, t = 8 * (lt % 8);
+        const bool all = whole<true>(cols, n, vec);
+        const uint4 w0 = all ? whole_octet<true>(p, s, 2 * cp, t, cols, n) : octet<true>(p, s, 2 * cp, t, cols, n, vec);
+        const uint4 w1 = all ? whole_octet<true>(p, s, 2 * cp + 1, t, cols, n) : octet<true>(p, s, 2 * cp + 1, t, cols, n, vec);
+        const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint32_t*>(&v[t + j][2 * cp]) = __byte_perm(u0[j >> 1], u1[j >> 1], (j & 1) ? 0x7632 : 0x5410);
+    }
+}
+
+template <int DK, bool FIRST>
+__global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_narrow(ChunkArgs x) {
+    using Sm = NarrowSmem<DK>;
+    constexpr int P = FIRST ? 8 : DK / 8, kTiles = DK / 16;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+    const DeltaArgs& a = x.a;
+    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int h = int(blockIdx.y), d0 = int(blockIdx.x) * kNarrowCols;
+    const int64_t b = blockIdx.z;
+    const int64_t len = length_of(a, b);
+    const int chunks = int((len + C - 1) / C);
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(&sm.full[s], kLoaders + 1);
+            tc::mbar_init(&sm.empty[s], kNarrowWarps);
+        }
+    }
+    __syncthreads();
+    if (warp >= kNarrowWarps) {
+        const int lt = tid - 32 * kNarrowWarps, cols = min(kNarrowCols, a.dv - d0);
+        run_loaders<DK, FIRST>(sm, x, lt, lane, h, b, len, d0, [&](typename Sm::Stage& st, const bf16* p, int n) {
+            load_values_narrow<FIRST>(st.v, p, a.vs, cols, n, x.vec_v, lt);
+        });
+        return;
+    }
+    const int g = lane >> 2, t4 = lane & 3;
+    const int dw = d0 + 8 * warp;                  // this warp's first channel
+    const int64_t sb = (b * a.Hv + h) * int64_t(a.dk) * a.dv;
+    float S[kTiles][4];
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * j + g + 8 * (i >> 1), d = dw + 2 * t4 + (i & 1);
+            S[j][i] = (a.state_in && d < a.dv && r < a.dk) ? a.state_in[sb + int64_t(r) * a.dv + d] : 0.0f;
+        }
+    bf16* ob = static_cast<bf16*>(a.o) + b * a.os.sb + (int64_t(h) * a.dv + dw) * a.os.sc;
+    bf16* so = sm.o[warp];
+    for (int ch = 0; ch < chunks; ++ch) {
+        const int s = ch & 1;
+        typename Sm::Stage& st = sm.st[s];
+        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) {
+            if (lane == 0) report_status(x.status, kStatusTimeout);
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
+            break;
+        }
+        const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
+        const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
+        float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            m0 = fmaxf(m0, fmaxf(fabsf(S[j][0]), fabsf(S[j][2])));
+            m1 = fmaxf(m1, fmaxf(fabsf(S[j][1]), fabsf(S[j][3])));
+        }
+        const Pow2 ps0(column_max(m0)), ps1(column_max(m1));
+        float X[4][4], O[4][4], U[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) X[i][j] = O[i][j] = U[i][j] = 0.0f;
+        // X = K S, O = Q S: left operands a step (three products) ahead
+        auto rows = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+            if constexpr (FIRST) {
+                left_km<P>(r, tk, step % 4, step / 4, lane);
+                left_km<P>(w, tq, step % 4, step / 4, lane);
+            } else {
+                left_mk<P>(r, tk, step % 4, step / 4, lane);
+                left_mk<P>(w, tq, step % 4, step / 4, lane);
+            }
+        };
+        {
+            uint32_t r[2][4], w[2][4];
+            rows(r[0], w[0], 0);
+#pragma unroll
+            for (int ks = 0; ks < kTiles; ++ks) {
+                const Right y(S[ks], ps0.up, ps1.up);
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const int step = 4 * ks + mt, at = step & 1;
+                    if (step + 1 < 4 * kTiles) rows(r[at ^ 1], w[at ^ 1], step + 1);
+                    mma_f16(X[mt], r[at], y.hi[0], y.hi[1]);
+                    mma_f16(O[mt], w[at], y.hi[0], y.hi[1]);
+                    mma_f16(X[mt], r[at], y.lo[0], y.lo[1]);
+                }
+            }
+        }
+        m0 = m1 = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const int t = 16 * mt + g;
+            const float cx0 = f.cx[t], cx1 = f.cx[t + 8], co0 = f.co[t], co1 = f.co[t + 8];
+            const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&st.v[t][8 * warp + 2 * t4]);
+            const uint32_t v1 = *reinterpret_cast<const uint32_t*>(&st.v[t + 8][8 * warp + 2 * t4]);
+            X[mt][0] = fmaf(-X[mt][0] * ps0.down, cx0, bf(v0, 0));
+            X[mt][1] = fmaf(-X[mt][1] * ps1.down, cx0, bf(v0, 1));
+            X[mt][2] = fmaf(-X[mt][2] * ps0.down, cx1, bf(v1, 0));
+            X[mt][3] = fmaf(-X[mt][3] * ps1.down, cx1, bf(v1, 1));
+            m0 = fmaxf(m0, fmaxf(fabsf(X[mt][0]), fabsf(X[mt][2])));
+            m1 = fmaxf(m1, fmaxf(fabsf(X[mt][1]), fabsf(X[mt][3])));
+            O[mt][0] = O[mt][0] * ps0.down * co0;
+            O[mt][1] = O[mt][1] * ps1.down * co0;
+            O[mt][2] = O[mt][2] * ps0.down * co1;
+            O[mt][3] = O[mt][3] * ps1.down * co1;
+        }
+        const Pow2 pr0(column_max(m0)), pr1(column_max(m1));
+        // U = T R, blocks on and under the diagonal
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const Right y(X[ks], pr0.up, pr1.up);
+#pragma unroll
+            for (int mt = ks; mt < 4; ++mt) {
+                uint32_t r[4], w[4];
+                left_mk<8>(r, tb, mt, ks, lane);
+                left_mk<8>(w, tb + kTile, mt, ks, lane);
+                mma_f16(U[mt], r, y.hi[0], y.hi[1]);
+                mma_f16(U[mt], r, y.lo[0], y.lo[1]);
+                mma_f16(U[mt], w, y.hi[0], y.hi[1]);
+            }
+        }
+        m0 = m1 = 0.0f;
+        float n0 = 0.0f, n1 = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const int t = 16 * mt + g;
+            const float ct0 = f.ct[t], ct1 = f.ct[t + 8], cu0 = f.cu[t], cu1 = f.cu[t + 8];
+            U[mt][0] = U[mt][0] * pr0.down * ct0;
+            U[mt][1] = U[mt][1] * pr1.down * ct0;
+            U[mt][2] = U[mt][2] * pr0.down * ct1;
+            U[mt][3] = U[mt][3] * pr1.down * ct1;
+            m0 = fmaxf(m0, fmaxf(fabsf(U[mt][0]), fabsf(U[mt][2])));
+            m1 = fmaxf(m1, fmaxf(fabsf(U[mt][1]), fabsf(U[mt][3])));
+            X[mt][0] = U[mt][0] * cu0;
+            X[mt][1] = U[mt][1] * cu0;
+            X[mt][2] = U[mt][2] * cu1;
+            X[mt][3] = U[mt][3] * cu1;
+            n0 = fmaxf(n0, fmaxf(fabsf(X[mt][0]), fabsf(X[mt][2])));
+            n1 = fmaxf(n1, fmaxf(fabsf(X[mt][1]), fabsf(X[mt][3])));
+        }
+        const Pow2 pu0(column_max(m0)), pu1(column_max(m1)), pw0(column_max(n0)), pw1(column_max(n1));
+        // S = gamma S + K^T (diag(cu) U), two tiles of key channels at a time
+        {
+            const Right y[4] = {{X[0], pw0.up, pw1.up}, {X[1], pw0.up, pw1.up}, {X[2], pw0.up, pw1.up}, {X[3], pw0.up, pw1.up}};
+            auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+                const int i = 2 * (step / 4), ks = step % 4;
+                if constexpr (FIRST) {
+                    left_mk<P>(r, tk, i, ks, lane);
+                    left_mk<P>(w, tk, i + 1, ks, lane);
+                } else {
+                    left_km<P>(r, tk, i, ks, lane);
+                    left_km<P>(w, tk, i + 1, ks, lane);
+                }
+            };
+            const float gamma = f.gamma;
+            uint32_t r[2][4], w[2][4];
+            keys_t(r[0], w[0], 0);
+            float D[4][4];
+#pragma unroll
+            for (int step = 0; step < 2 * kTiles; ++step) {
+                const int i = 2 * (step / 4), ks = step % 4, at = step & 1;
+                if (step + 1 < 2 * kTiles) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
+                if (ks == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) D[0][j] = D[1][j] = D[2][j] = D[3][j] = 0.0f;
+                }
+                mma_f16(D[0], r[at], y[ks].hi[0], y[ks].hi[1]);
+                mma_f16(D[1], w[at], y[ks].hi[0], y[ks].hi[1]);
+                mma_f16(D[2], r[at], y[ks].lo[0], y[ks].lo[1]);
+                mma_f16(D[3], w[at], y[ks].lo[0], y[ks].lo[1]);
+                if (ks == 3) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float down = (j & 1) ? pw1.down : pw0.down;
+                        S[i][j] = fmaf(gamma, S[i][j], (D[0][j] + D[2][j]) * down);
+                        S[i + 1][j] = fmaf(gamma, S[i + 1][j], (D[1][j] + D[3][j]) * down);
+                    }
+                }
+            }
+        }
+        // O += P U
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t u0 = transposed(pack_h(U[ks][0] * pu0.up, U[ks][1] * pu1.up));
+            const uint32_t u1 = transposed(pack_h(U[ks][2] * pu0.up, U[ks][3] * pu1.up));
+#pragma unroll
+            for (int mt = ks; mt < 4; ++mt) {
+                uint32_t r[4];
+                left_mk<8>(r, tb + 2 * kTile, mt, ks, lane);
+                mma_f16(X[mt], r, u0, u1);
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const int t = 16 * mt + g;
+            const float cp0 = f.cp[t], cp1 = f.cp[t + 8];
+            const uint32_t y0 = tc::pack2(fmaf(X[mt][0] * pu0.down, cp0, O[mt][0]), fmaf(X[mt][1] * pu1.down, cp0, O[mt][1]));
+            const uint32_t y1 = tc::pack2(fmaf(X[mt][2] * pu0.down, cp1, O[mt][2]), fmaf(X[mt][3] * pu1.down, cp1, O[mt][3]));
+            if constexpr (FIRST) {
+                // rows are channels: the blocks transposed
+                *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 2 * t4) = transposed(y0);
+                *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 8 + 2 * t4) = transposed(y1);
+            } else {
+                *reinterpret_cast<uint32_t*>(so + t * 8 + 2 * t4) = y0;
+                *reinterpret_cast<uint32_t*>(so + (t + 8) * 8 + 2 * t4) = y1;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+        const int64_t t0 = int64_t(ch) * C;
+        const int n = int(min(int64_t(C), len - t0)), cols = min(8, a.dv - dw);
+        bf16* oc = ob + t0 * a.os.st;
+        if (x.vec_o && n == C && cols == 8) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = lane + 32 * j;
+                if constexpr (FIRST)
+                    *reinterpret_cast<uint4*>(oc + int64_t(i >> 3) * a.os.sc + (i & 7) * 8) =
+                        *reinterpret_cast<const uint4*>(so + (i >> 3) * kVRow + (i & 7) * 8);
+                else
+                    *reinterpret_cast<uint4*>(oc + int64_t(i) * a.os.st) = *reinterpret_cast<const uint4*>(so + i * 8);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = lane; i < 8 * C; i += 32) {
+                // the output's contiguous axis over neighbouring lanes
+                const int c = FIRST ? i / C : i % 8, t = FIRST ? i % C : i / 8;
+                if (c < cols && t < n) oc[int64_t(c) * a.os.sc + int64_t(t) * a.os.st] = FIRST ? so[c * kVRow + t] : so[t * 8 + c];
+            }
+        }
+        __syncwarp();
+    }
+    if (a.state_out) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * j + g + 8 * (i >> 1), d = dw + 2 * t4 + (i & 1);
+                if (d < a.dv && r < a.dk) a.state_out[sb + int64_t(r) * a.dv + d] = S[j][i];
+            }
+    }
+}
+
 // --------------------------------------------------------------------- host
 // Eight elements along the contiguous axis as one 16-byte access, wherever a row starts.
 bool vec_ok(const void* p, const DeltaView& s, bool first, int head_channels) {
@@ -958,11 +1294,24 @@ cudaError_t launch_scan(const ChunkArgs& x, cudaStream_t s) {
 }
 
 template <int DK, bool FIRST>
+cudaError_t launch_narrow(const ChunkArgs& x, cudaStream_t s) {
+    const size_t bytes = sizeof(NarrowSmem<DK>);
+    static std::atomic<bool> raised[kMaxDevices];
+    cudaError_t e = raise_smem(k_delta_scan_narrow<DK, FIRST>, bytes, x.dev, raised);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(unsigned((x.a.dv + kNarrowCols - 1) / kNarrowCols), unsigned(x.a.Hv), unsigned(x.a.B));
+    k_delta_scan_narrow<DK, FIRST><<<grid, 32 * kNarrowWarps + kLoaders, bytes, s>>>(x);
+    return cudaGetLastError();
+}
+
+template <int DK, bool FIRST>
 cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
     cudaError_t e = launch_prep<DK, FIRST>(x, s);
     if (e != cudaSuccess) return e;
-    // four warps have a scheduler each; eight share them, which pays once half-width CTAs would not all be resident
-    const int64_t ctas = x.a.B * x.a.Hv * ((x.a.dv + 63) / 64);
+    // Narrow CTAs (32 channels) while every one of them has an SM; then four warps of 16 channels, a scheduler each; eight
+    // share them, which pays once half-width CTAs would not all be resident.
+    const int64_t heads = x.a.B * x.a.Hv, ctas = heads * ((x.a.dv + 63) / 64);
+    if (heads * ((x.a.dv + kNarrowCols - 1) / kNarrowCols) <= x.sms) return launch_narrow<DK, FIRST>(x, s);
     return ctas <= x.sms ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
 }
 

@@ -115,6 +115,9 @@ SHAPES = [
     (1, 1, 1, 1, 16, 16), (2, 2, 1, 2, 64, 64), (1, 17, 2, 2, 64, 64), (2, 63, 1, 1, 128, 128), (1, 64, 2, 4, 128, 128),
     (2, 65, 1, 1, 128, 64), (1, 128, 3, 3, 64, 96), (1, 200, 1, 3, 100, 40), (2, 129, 2, 2, 40, 24), (1, 300, 1, 1, 128, 160),
     (1, 96, 1, 2, 1, 1), (1, 70, 1, 1, 7, 256), (1, 512, 2, 2, 128, 128),
+    # heads enough for the wider scans: one, then two warps a scheduler
+    (20, 130, 2, 4, 64, 64), (10, 200, 2, 4, 128, 128), (10, 70, 4, 4, 100, 120),
+    (40, 70, 2, 4, 64, 64), (19, 130, 2, 4, 128, 128), (40, 65, 4, 4, 100, 120),
 ]
 
 
@@ -350,7 +353,7 @@ def test_long_sequence_sampled():
 
 # ------------------------------------------------------------------------ step
 @pytest.mark.parametrize("B,Hk,Hv,dk,dv", [(1, 1, 1, 128, 128), (3, 2, 4, 64, 96), (2, 1, 3, 100, 40), (5, 1, 1, 7, 33),
-                                           (2, 2, 2, 1, 1), (1, 1, 1, 128, 256), (70, 1, 2, 64, 64)])
+                                           (2, 2, 2, 1, 1), (1, 1, 1, 128, 256), (70, 1, 2, 64, 64), (160, 2, 2, 128, 100)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("l2norm", [True, False])
 def test_step(B, Hk, Hv, dk, dv, dtype, l2norm):
