@@ -135,22 +135,17 @@ __device__ __forceinline__ float quad_max(float v) {
 
 __device__ __forceinline__ float bf(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xffff0000u) : (w << 16)); }
 
-// Eight elements of a [channel, time] view from (c, t), along time (FIRST) or along channels; what lies outside
-// [0, nc) x [0, nt) is zero and not read.  vec: eight elements of a row inside the view are one aligned load.
+// Eight elements of a [channel, time] view from (c, t), along time (FIRST) or along channels, one by one; what lies
+// outside [0, nc) x [0, nt) is zero and not read.  No branches, so that the loads of several go out together.
 template <bool FIRST>
-__device__ __forceinline__ uint4 octet(const bf16* p, const DeltaView& s, int c, int t, int nc, int nt, bool vec) {
+__device__ __forceinline__ uint4 octet(const bf16* p, const DeltaView& s, int c, int t, int nc, int nt) {
     const bf16* at = p + int64_t(c) * s.sc + int64_t(t) * s.st;
     const int n = FIRST ? (c < nc ? nt - t : 0) : (t < nt ? nc - c : 0);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (n >= 8 && vec) return __ldg(reinterpret_cast<const uint4*>(at));
-    if (n > 0) {
-        const int64_t step = FIRST ? s.st : s.sc;
-        uint32_t h[8];
+    const int64_t step = FIRST ? s.st : s.sc;
+    uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = i < n ? uint32_t(__ldg(reinterpret_cast<const unsigned short*>(at + i * step))) : 0u;
-        w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
-    return w;
+    for (int i = 0; i < 8; ++i) h[i] = i < n ? uint32_t(__ldg(reinterpret_cast<const unsigned short*>(at + i * step))) : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
 // Whether all octets of a [nc] x [nt] tile lie inside it or outside it as wholes, and load as such: then a thread's
@@ -275,12 +270,12 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             copy_octet<FIRST>(sm.q + piece<P>(row, c), qp, a.qs, FIRST ? row : 8 * c, FIRST ? 8 * c : row, a.dk, n);
         }
     } else {
-#pragma unroll 1
+#pragma unroll 2
         for (int i = tid; i < Sm::kRows * P; i += kPrepThreads) {
             const int row = i / P, c = i % P;
             const int ch = FIRST ? row : 8 * c, tt = FIRST ? 8 * c : row;
-            *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = octet<FIRST>(kp, a.ks, ch, tt, a.dk, n, x.vec_k);
-            *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n, x.vec_q);
+            *reinterpret_cast<uint4*>(sm.k + piece<P>(row, c)) = octet<FIRST>(kp, a.ks, ch, tt, a.dk, n);
+            *reinterpret_cast<uint4*>(sm.q + piece<P>(row, c)) = octet<FIRST>(qp, a.qs, ch, tt, a.dk, n);
         }
     }
     cp_async_commit();
@@ -510,10 +505,10 @@ __device__ __forceinline__ void load_tile(uint8_t* tile, const bf16* p, const De
             copy_octet<FIRST>(tile + piece<P>(row, c), p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n);
         }
     } else {
-#pragma unroll 1
+#pragma unroll 2
         for (int i = lt; i < C * DK / 8; i += kLoaders) {
             const int row = i / P, c = i % P;
-            *reinterpret_cast<uint4*>(tile + piece<P>(row, c)) = octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n, vec);
+            *reinterpret_cast<uint4*>(tile + piece<P>(row, c)) = octet<FIRST>(p, s, FIRST ? row : 8 * c, FIRST ? 8 * c : row, dk, n);
         }
     }
 }
@@ -546,7 +541,7 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
             }
         } else {
 #pragma unroll 1
-            for (int i = lt; i < 16 * NW * 8; i += kLoaders) put(i, octet<true>(p, s, i / 8, 8 * (i % 8), cols, n, vec));
+            for (int i = lt; i < 16 * NW * 8; i += kLoaders) put(i, octet<true>(p, s, i / 8, 8 * (i % 8), cols, n));
         }
     } else {
         // neighbouring lanes: neighbouring octets of a token's row, so whole sectors are read
@@ -571,8 +566,8 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
         } else {
 #pragma unroll 1
             for (int i = lt; i < 32 * kRowOct; i += kLoaders)
-                put(i, octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct), cols, n, vec),
-                    octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct) + 1, cols, n, vec));
+                put(i, octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct), cols, n),
+                    octet<false>(p, s, 8 * (i % kRowOct), 2 * (i / kRowOct) + 1, cols, n));
         }
     }
 }
@@ -999,17 +994,17 @@ __device__ __forceinline__ void load_values_narrow(bf16 (&v)[C][kNarrowVRow], co
                 copy_octet<false>(&v[i / kRowOct][8 * (i % kRowOct)], p, s, 8 * (i % kRowOct), i / kRowOct, cols, n);
             }
         } else {
-#pragma unroll 1
+#pragma unroll 2
             for (int i = lt; i < C * kRowOct; i += kLoaders)
                 *reinterpret_cast<uint4*>(&v[i / kRowOct][8 * (i % kRowOct)]) =
-                    octet<false>(p, s, 8 * (i % kRowOct), i / kRowOct, cols, n, vec);
+                    octet<false>(p, s, 8 * (i % kRowOct), i / kRowOct, cols, n);
         }
     } else {
         static_assert(kNarrowCols / 2 * 8 == kLoaders, "a pair of octets a thread");
         const int cp = lt / 8, t = 8 * (lt % 8);
         const bool all = whole<true>(cols, n, vec);
-        const uint4 w0 = all ? whole_octet<true>(p, s, 2 * cp, t, cols, n) : octet<true>(p, s, 2 * cp, t, cols, n, vec);
-        const uint4 w1 = all ? whole_octet<true>(p, s, 2 * cp + 1, t, cols, n) : octet<true>(p, s, 2 * cp + 1, t, cols, n, vec);
+        const uint4 w0 = all ? whole_octet<true>(p, s, 2 * cp, t, cols, n) : octet<true>(p, s, 2 * cp, t, cols, n);
+        const uint4 w1 = all ? whole_octet<true>(p, s, 2 * cp + 1, t, cols, n) : octet<true>(p, s, 2 * cp + 1, t, cols, n);
         const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int j = 0; j < 8; ++j)

@@ -8,11 +8,13 @@
 // P in fp32 and the CUDA cores add it, scaled, to fp32 sums in registers.
 //
 // k_proj_fp8 (more than kFewTokens rows): persistent, 384 threads a CTA in
-// three roles:
+// four roles:
 //   warp 0      TMA: x and W blocks of 128 bytes a row (128-byte swizzle) into a
 //               ring of stages;
 //   warp 1      tcgen05.mma kind::f8f6f4 (K 32; four a block) into one of two
 //               tensor-memory buffers, a commit per block;
+//   warps 2, 3  the rows' factors xs Ws of each block into shared memory, their
+//               loads four blocks ahead;
 //   warps 4-11  two warpgroups, half of the columns each (their sums take most
 //               of the registers, which the first warpgroup hands over): read a
 //               block's P with tcgen05.ld as fragments, free the buffer, add it
@@ -37,7 +39,7 @@
 
 #include <string>
 
-#include "common.cuh"
+
 #include "hyena.h"
 #include "kernels.h"
 #include "tc_util.cuh"
@@ -54,7 +56,6 @@ using bf16 = __nv_bfloat16;
 constexpr int BM = 128, BKB = 128;                // rows of a CTA's tile, bytes of a block
 constexpr int kThreads = 384;
 constexpr uint32_t kATile = BM * BKB;
-constexpr int kRing = 8, kAhead = 7;              // scales in flight
 
 // How a tile leaves: element by element, or as TMA stores of the tensor map `map_o`.
 enum Store { STORE_PLAIN = 0, STORE_TMA = 1 };
@@ -81,7 +82,7 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = 2 * BN;
     static constexpr int CW = BN / 2;             // columns a consuming thread
     static constexpr uint32_t kOutWarp = 32 * CW * 2;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 8 * kOutWarp + 512 + 8 * CW * 4 + 2 * kRing * 256 * 4;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 8 * kOutWarp + 512 + 8 * CW * 4 + kStages * 256 * 4;
 };
 
 // Neighbouring tiles at work together lie along the output's contiguous axis.
@@ -213,14 +214,14 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     uint8_t* stages = smem_p + ((1024u - (tc::smem_u32(smem_p) & 1023u)) & 1023u);
     uint8_t* out_stage = stages + kStages * kStageBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + 8 * Cf::kOutWarp);
-    uint64_t* done = full + kStages;              // a stage's products: it is free, and its sums are there
+    uint64_t* done = full + kStages;              // a stage's products and factors: it is free, and its sums are there
     uint64_t* acc_empty = done + kStages;         // [buffer]
     uint64_t* out_full = acc_empty + 2;           // [half]: its four warps have staged their part
     uint64_t* out_free = out_full + 2;            // [half]: the staging has been read
     uint64_t* mma_done = out_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     float* s_bias = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 512);
-    float* s_ring = s_bias + 8 * CW;
+    float* s_fac = s_bias + 8 * CW;               // [stage][half][32 q + 4 (row % 8) + row / 8]: a thread's four rows together
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = int(threadIdx.x) & 31;
     const int rank = G == 2 ? int(blockIdx.x) & 1 : 0;             // in the pair; the first issues the products
@@ -228,7 +229,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&done[s], 1);
+            tc::mbar_init(&done[s], 3);           // the products, and two warps' factors
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(&acc_empty[a], 8 * G);  // one arrival a reading warp
@@ -245,9 +246,9 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     const uint32_t tmem = *tmem_slot;
     const int tiles = p.tiles_m * p.tiles_n;
 
-    // registers: 384 x 168 at launch = 128 x 40 + 256 x 232
+    // registers: 384 x 168 at launch = 128 x 56 + 256 x 224
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
         // one thread each: stage and buffer counters step, nothing is divided, so that issuing stays under the products
         if (warp == 0 && lane == 0) {
             int s = 0, issued = 0;
@@ -333,45 +334,84 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             if (elect_one()) commit<G>(mma_done);
             __syncwarp();
             if (!tc::mbar_wait(mma_done, 0, p.budget_ns) && lane == 0) report_status(p.status, kStatusTimeout);
+        } else if (warp >= 2) {
+            // The factors xs Ws of this CTA's rows, two rows a thread, for both halves of the columns.  The loads go out four
+            // blocks ahead (registers of a static index), across tiles.
+            const int t = int(threadIdx.x) - 64, total = (tiles - first + step - 1) / step * p.kblocks;
+            float x0[4], x1[4], w0[4], w1[4];
+            int pt = first, pkb = p.kblocks;      // the tile and block to load next
+            const float *px0 = nullptr, *px1 = nullptr, *pw0 = nullptr, *pw1 = nullptr;
+            bool in0 = false, in1 = false, has0 = false, has1 = false;
+            auto load = [&](int u) {
+                if (pkb == p.kblocks) {           // enter tile pt
+                    int tm, tn;
+                    place(p, pt, tm, tn);
+                    const uint32_t m = (uint32_t(tm) * G + rank) * BM + t;
+                    const int64_t n = int64_t(tn) * BN;
+                    const bool more = pt < tiles;
+                    in0 = more && m < p.M;
+                    in1 = more && m + 64 < p.M;
+                    has0 = more && n < p.N;
+                    has1 = more && n + CW < p.N;
+                    // row m of batch row b: xs + (b kblocks + kb) L + m - b L
+                    px0 = p.xs + int64_t(in0 ? m / uint32_t(p.L) : 0) * (p.kblocks - 1) * p.L + m;
+                    px1 = p.xs + int64_t(in1 ? (m + 64) / uint32_t(p.L) : 0) * (p.kblocks - 1) * p.L + m + 64;
+                    pw0 = p.ws + n / 128 * p.kblocks;
+                    pw1 = p.ws + (n + CW) / 128 * p.kblocks;
+                    pt += step;
+                    pkb = 0;
+                }
+                x0[u] = in0 ? __ldg(px0) : 0.0f;
+                x1[u] = in1 ? __ldg(px1) : 0.0f;
+                w0[u] = has0 ? __ldg(pw0) : 0.0f;
+                w1[u] = has1 ? __ldg(pw1) : 0.0f;
+                px0 += p.L;
+                px1 += p.L;
+                ++pw0;
+                ++pw1;
+                ++pkb;
+            };
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load(u);
+            const int at = 32 * (t >> 5) + 4 * (t & 7) + ((t & 31) >> 3);
+            // A stage's factors have been read once the sums' buffer of its block, freed by their readers, has been filled
+            // by the block two later; so `done` of the block kStages - 2 before is waited for.
+            int s = 0, sw = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int j0 = 0; j0 < total && ok; j0 += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j0 + u < total && ok) {
+                        if (j0 + u >= kStages - 2) {
+                            ok = tc::mbar_wait(&done[sw], phase, p.budget_ns);
+                            if (++sw == kStages) {
+                                sw = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        float* f = s_fac + s * 256 + at;
+                        f[0] = x0[u] * w0[u];
+                        f[64] = x1[u] * w0[u];
+                        f[128] = x0[u] * w1[u];
+                        f[192] = x1[u] * w1[u];
+                        load(u);
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&done[s]);
+                        if (++s == kStages) s = 0;
+                    }
+                }
+            }
+            if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t t_col = tmem + uint32_t(half * CW) + (uint32_t(32 * q) << 16);
         uint8_t* stage = out_stage + (warp - 4) * Cf::kOutWarp;     // (channels_first: a half's four parts together)
         float* bias = s_bias + (warp - 4) * CW;
-        // The scales come kAhead blocks ahead (a block's products take less than a load under traffic), across tiles, by
-        // asynchronous 4-byte copies into a ring of the warp's own, row `lane` by this lane.
-        float2* ring = reinterpret_cast<float2*>(s_ring) + 32 * (warp - 4);
-        int pt = first, pc = 0, pkb = p.kblocks;  // the tile, the ring's slot and the block to fetch next
-        const float *px = nullptr, *pw = nullptr;
-        bool plive = false;
-        auto fetch = [&]() {
-            if (pkb == p.kblocks) {               // enter tile pt
-                int tm, tn;
-                place(p, pt, tm, tn);
-                const uint32_t m = (uint32_t(tm) * G + rank) * BM + 32 * q + lane;
-                const int64_t n = int64_t(tn) * BN + half * CW;
-                plive = pt < tiles && m < p.M && n < p.N;
-                const int64_t b = plive ? m / uint32_t(p.L) : 0;
-                px = p.xs + b * (p.kblocks - 1) * p.L + (plive ? m : 0);
-                pw = p.ws + (plive ? n / 128 : 0) * p.kblocks;
-                pt += step;
-                pkb = 0;
-            }
-            if (plive) {
-                cp_async_small<4>(&ring[pc + lane].x, px);
-                cp_async_small<4>(&ring[pc + lane].y, pw);
-            }
-            cp_async_commit();
-            px += p.L;
-            ++pw;
-            ++pkb;
-            pc = (pc + 256) & (kRing * 256 - 1);
-        };
-#pragma unroll 1
-        for (int i = 0; i < kAhead; ++i) fetch();
-        int buf = 0, slot = 0, s = 0;
+        int buf = 0, s = 0;
         uint32_t phase = 0, out_phase = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -401,17 +441,12 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 constexpr int kPieces = CW / 16;
                 float v[2][16];
                 tmem_ld_frag(t_col + uint32_t(buf * BN), v[0]);
-                asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
-                __syncwarp();
+                const float4 fac = *reinterpret_cast<const float4*>(s_fac + s * 256 + half * 128 + 32 * q + 4 * (lane >> 2));
                 uint64_t f2[4];                   // of rows g + 8 i
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 sc = ring[slot + (lane >> 2) + 8 * i];
-                    const float f = m0 + (lane >> 2) + 8 * i < p.M && n0 < p.N ? sc.x * sc.y : 0.0f;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(f2[i]) : "f"(f));
-                }
-                slot = (slot + 256) & (kRing * 256 - 1);
-                fetch();
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[0]) : "f"(fac.x));
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[1]) : "f"(fac.y));
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[2]) : "f"(fac.z));
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[3]) : "f"(fac.w));
 #pragma unroll
                 for (int c = 0; c < kPieces; ++c) {
                     tc::tmem_ld_wait();
@@ -536,7 +571,6 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             }
         }
         if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
-        cp_async_wait_all();
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
     __syncwarp();

@@ -98,14 +98,14 @@ __device__ __forceinline__ uint2 quotients8(const Scale& sc, const float (&v)[8]
 }
 
 // x [rows of K], channels contiguous: 16 lanes take a block of 128 as eight
-// values each; a CTA takes 64 rows of one block, so its 64 scales leave as one
+// values each; a CTA takes 32 rows of one block, so its 32 scales leave as one
 // contiguous store.
-constexpr int kRowsLast = 64;
+constexpr int kRowsLast = 32, kThreadsLast = 128;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
+__global__ void __launch_bounds__(kThreadsLast, sizeof(T) == 2 ? 12 : 8)
 k_quant_last(const T* __restrict__ x, uint8_t* __restrict__ xq, float* __restrict__ xs, int64_t L, int64_t K) {
-    constexpr int kIter = kRowsLast / (kThreads / 16);
+    constexpr int kIter = kRowsLast / (kThreadsLast / 16), kStep = kThreadsLast / 16;
     __shared__ float s_scale[kRowsLast];
     const int64_t kb = blockIdx.x, l0 = int64_t(blockIdx.y) * kRowsLast, b = blockIdx.z;
     const int g = int(threadIdx.x) >> 4, lane = int(threadIdx.x) & 15;
@@ -113,7 +113,7 @@ k_quant_last(const T* __restrict__ x, uint8_t* __restrict__ xq, float* __restric
     Octet<T> w[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int64_t l = l0 + g + 16 * i;
+        const int64_t l = l0 + g + kStep * i;
         if (l < L && c < K) w[i].load(x + (b * L + l) * K + c);
         else w[i].zero();
     }
@@ -127,9 +127,9 @@ k_quant_last(const T* __restrict__ x, uint8_t* __restrict__ xq, float* __restric
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
         const Scale sc(m);
-        const int64_t l = l0 + g + 16 * i;
+        const int64_t l = l0 + g + kStep * i;
         if (l < L && c < K) *reinterpret_cast<uint2*>(xq + (b * L + l) * K + c) = quotients8(sc, v);
-        if (lane == 0) s_scale[g + 16 * i] = sc.s;
+        if (lane == 0) s_scale[g + kStep * i] = sc.s;
     }
     __syncthreads();
     if (threadIdx.x < kRowsLast && l0 + threadIdx.x < L)
@@ -268,20 +268,20 @@ extern "C" hyena_status_t hyena_quantize_fp8(const void* x, void* xq, float* xs,
     if (B < 1 || L < 1 || K < 1) return fail(HYENA_ERR_INVALID_ARG, "B, L and K must be >= 1");
     if (K % 16 != 0 || K > (int64_t(1) << 20) || B > 65535 || B * L > (int64_t(1) << 31) - 1 || L > kRowsLast * int64_t(65535))
         return fail(HYENA_ERR_UNSUPPORTED_SHAPE,
-                    "K must be a multiple of 16 up to 2^20, B <= 65535, L <= 64 * 65535 and B * L < 2^31");
+                    "K must be a multiple of 16 up to 2^20, B <= 65535, L <= 32 * 65535 and B * L < 2^31");
     const int64_t nb = (K + kBlk - 1) / kBlk;
     hyena_status_t st = check(x, xq, xs, B * L, K, B * nb * L, dtype);
     if (st != HYENA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* q = static_cast<uint8_t*>(xq);
-    static_assert(kRowsLast == kPosFirst, "one grid for both layouts");
-    const dim3 grid(unsigned(nb), unsigned((L + kRowsLast - 1) / kRowsLast), unsigned(B));
+    const int rows = channels_first ? kPosFirst : kRowsLast;
+    const dim3 grid(unsigned(nb), unsigned((L + rows - 1) / rows), unsigned(B));
     if (channels_first) {
         if (dtype == HYENA_BF16) k_quant_first<<<grid, kThreads, 0, s>>>(static_cast<const bf16*>(x), q, xs, L, K, L % 8 == 0);
         else k_quant_first<<<grid, kThreads, 0, s>>>(static_cast<const float*>(x), q, xs, L, K, L % 4 == 0);
     } else {
-        if (dtype == HYENA_BF16) k_quant_last<<<grid, kThreads, 0, s>>>(static_cast<const bf16*>(x), q, xs, L, K);
-        else k_quant_last<<<grid, kThreads, 0, s>>>(static_cast<const float*>(x), q, xs, L, K);
+        if (dtype == HYENA_BF16) k_quant_last<<<grid, kThreadsLast, 0, s>>>(static_cast<const bf16*>(x), q, xs, L, K);
+        else k_quant_last<<<grid, kThreadsLast, 0, s>>>(static_cast<const float*>(x), q, xs, L, K);
     }
     return done(cudaGetLastError());
 }

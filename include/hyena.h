@@ -480,7 +480,7 @@ hyena_status_t hyena_delta_rule_step(const hyena_delta_rule_t* p, float* states,
  *   xs = max(amax / 448, 2^-126) over the block's |x|, xq = x / xs rounded to
  *   nearest even; amax / 448 and x / xs are fp32 numbers (round to nearest).
  * A block that holds an infinity or a NaN gets scale infinity or NaN, so every
- * value it stands for is NaN.  K a multiple of 16, B <= 65535; x, xq
+ * value it stands for is NaN.  K a multiple of 16 up to 2^20, B <= 65535, L <= 32 * 65535, B L < 2^31; x, xq
  * 16-byte aligned, xs 4-byte; outputs may not overlap x.
  */
 hyena_status_t hyena_quantize_fp8(const void* x, void* xq, float* xs, int64_t B, int64_t L, int64_t K,
