@@ -17,8 +17,8 @@
 //               loads four blocks ahead;
 //   warps 4-11  two warpgroups, half of the columns each (their sums take most
 //               of the registers, which the first warpgroup hands over): read a
-//               block's P with tcgen05.ld as fragments, free the buffer, add it
-//               times the rows' factors (four rows a thread).
+//               block's P with tcgen05.ld (a row a thread), free the buffer, add
+//               it times the row's factor.
 // Tiles.  Large products run on pairs of CTAs (cta_group::2): 256 x 256, each
 // CTA the sums of its 128 rows and half of the W rows in its shared memory, so
 // a block brings 32 KB into an SM for its 512 cycles of tensor work; a CTA by
@@ -174,14 +174,25 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&r)[16]) {
     for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(v[i]);
 }
 
-// Four 8 x 8 matrices of 16-bit numbers from fragments, rows as they are or transposed.
-__device__ __forceinline__ void stmatrix4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-                 : "memory");
-}
+// Four 8 x 8 matrices of 16-bit numbers from fragments, transposed.
 __device__ __forceinline__ void stmatrix4_trans(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                  : "memory");
+}
+
+// 32 lanes x 32 columns, row `lane` from this lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint64_t (&v)[16]) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm("mov.b64 {%0, %1}, %2;" : "=r"(r[2 * i]), "=r"(r[2 * i + 1]) : "l"(v[i]));
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -221,7 +232,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
     uint64_t* mma_done = out_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     float* s_bias = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 512);
-    float* s_fac = s_bias + 8 * CW;               // [stage][half][32 q + 4 (row % 8) + row / 8]: a thread's four rows together
+    float* s_fac = s_bias + 8 * CW;               // [stage][half][row]
 
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = int(threadIdx.x) & 31;
     const int rank = G == 2 ? int(blockIdx.x) & 1 : 0;             // in the pair; the first issues the products
@@ -373,7 +384,6 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             };
 #pragma unroll
             for (int u = 0; u < 4; ++u) load(u);
-            const int at = 32 * (t >> 5) + 4 * (t & 7) + ((t & 31) >> 3);
             // A stage's factors have been read once the sums' buffer of its block, freed by their readers, has been filled
             // by the block two later; so `done` of the block kStages - 2 before is waited for.
             int s = 0, sw = 0;
@@ -391,7 +401,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                                 phase ^= 1u;
                             }
                         }
-                        float* f = s_fac + s * 256 + at;
+                        float* f = s_fac + s * 256 + t;
                         f[0] = x0[u] * w0[u];
                         f[64] = x1[u] * w0[u];
                         f[128] = x0[u] * w1[u];
@@ -421,15 +431,20 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             const int64_t n0 = int64_t(tn) * BN + half * CW;
             const bool live = m < p.M;
             const int64_t b = live ? uint32_t(m) / uint32_t(p.L) : 0, l = live ? m - b * p.L : 0;
-            // the bias of this warp's columns, its own copy: no barrier that a warp which gave up would leave others at
-            __syncwarp();
+            float bv[CW / 32];                    // the bias of this warp's columns, on its way under the products
 #pragma unroll
-            for (int i = lane; i < CW; i += 32) bias[i] = (p.bias && n0 + i < p.N) ? __ldg(p.bias + n0 + i) : 0.0f;
-            __syncwarp();
-            // sums as pairs of neighbouring columns: of rows g + 16 hh and g + 8 + 16 hh, columns 8 j + 2 t
-            uint64_t acc[2][CW / 8][2];
+            for (int i = 0; i < CW / 32; ++i) bv[i] = (p.bias && n0 + 32 * i + lane < p.N) ? __ldg(p.bias + n0 + 32 * i + lane) : 0.0f;
+            uint64_t acc[CW / 2];                 // pairs of neighbouring columns
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i) (&acc[0][0][0])[i] = 0;
+            for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
+            auto release = [&](int bf) {          // the warp has read buffer bf
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (G == 2) arrive_first(&acc_empty[bf]);
+                    else tc::mbar_arrive(&acc_empty[bf]);
+                }
+            };
 #pragma unroll 1
             for (int kb = 0; kb < p.kblocks; ++kb) {
                 if (!tc::mbar_wait(&done[s], phase, p.budget_ns)) {
@@ -437,36 +452,19 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     break;
                 }
                 tc::fence_after_sync();
-                // a piece of 16 rows x 32 columns loads under the multiply-adds of another, the first while the factors come
-                constexpr int kPieces = CW / 16;
+                // 16 columns load under the multiply-adds of 16, the first while the factor comes
                 float v[2][16];
-                tmem_ld_frag(t_col + uint32_t(buf * BN), v[0]);
-                const float4 fac = *reinterpret_cast<const float4*>(s_fac + s * 256 + half * 128 + 32 * q + 4 * (lane >> 2));
-                uint64_t f2[4];                   // of rows g + 8 i
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[0]) : "f"(fac.x));
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[1]) : "f"(fac.y));
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[2]) : "f"(fac.z));
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2[3]) : "f"(fac.w));
+                tc::tmem_ld16(t_col + uint32_t(buf * BN), v[0]);
+                const float f = s_fac[s * 256 + half * 128 + 32 * q + lane];
+                uint64_t f2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
 #pragma unroll
-                for (int c = 0; c < kPieces; ++c) {
+                for (int c = 0; c < CW / 16; ++c) {
                     tc::tmem_ld_wait();
-                    if (c + 1 < kPieces) {
-                        const int hh = (c + 1) / (CW / 32), cc = (c + 1) % (CW / 32);
-                        tmem_ld_frag(t_col + uint32_t(buf * BN + 32 * cc) + (uint32_t(16 * hh) << 16), v[(c + 1) & 1]);
-                    } else {
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (G == 2) arrive_first(&acc_empty[buf]);
-                            else tc::mbar_arrive(&acc_empty[buf]);
-                        }
-                    }
-                    const int hh = c / (CW / 32), cc = c % (CW / 32);
+                    if (c + 1 < CW / 16) tc::tmem_ld16(t_col + uint32_t(buf * BN + 16 * (c + 1)), v[(c + 1) & 1]);
+                    else if (!p.channels_first || kb + 1 < p.kblocks) release(buf);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        fma2(acc[hh][4 * cc + j][0], v[c & 1][4 * j], v[c & 1][4 * j + 1], f2[2 * hh]);
-                        fma2(acc[hh][4 * cc + j][1], v[c & 1][4 * j + 2], v[c & 1][4 * j + 3], f2[2 * hh + 1]);
-                    }
+                    for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f2);
                 }
                 buf ^= 1;
                 if (++s == kStages) {
@@ -479,6 +477,11 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     p.out[p.channels_first ? (b * p.N + n0 + i) * p.L + l : m * p.N + n0 + i] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
                 break;
             }
+            // the warp's own copy: no barrier that a warp which gave up would leave others at
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < CW / 32; ++i) bias[32 * i + lane] = bv[i];
+            __syncwarp();
             if (p.store == STORE_TMA) {
                 // the last tile's stores have read the staging
                 if (!p.channels_first || q == 0) {
@@ -495,28 +498,51 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
             // columns][row][kBox columns]; 128-byte swizzle (64-byte rows: 64-byte swizzle).
             constexpr int kBox = CW < 64 ? CW : 64;
             uint8_t* half_stage = out_stage + half * (4 * Cf::kOutWarp);
-            const int mat = lane >> 3, mr = lane & 7;
+            if (p.channels_first) {
+                // The sums go back to the last buffer, held until here, and come again as fragments, which stmatrix
+                // transposes: positions together.  (Reading every block as fragments costs twice the reading: 331 us
+                // against 277 us at 32768 x 2048 x 4096.)
+                const uint32_t t_buf = t_col + uint32_t((buf ^ 1) * BN);
 #pragma unroll
-            for (int j = 0; j < CW / 8; j += 2) {
-                const float2 b0 = *reinterpret_cast<const float2*>(bias + 8 * j + 2 * (lane & 3));
-                const float2 b1 = *reinterpret_cast<const float2*>(bias + 8 * j + 8 + 2 * (lane & 3));
+                for (int c = 0; c < CW / 2; c += 16) tmem_st32(t_buf + uint32_t(2 * c), *reinterpret_cast<const uint64_t(*)[16]>(acc + c));
+                asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+                const int mat = lane >> 3, mr = lane & 7;
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
+                for (int c = 0; c < CW / 32; ++c) {
+                    float v[2][16];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) tmem_ld_frag(t_buf + uint32_t(32 * c) + (uint32_t(16 * hh) << 16), v[hh]);
+                    tc::tmem_ld_wait();
+                    if (c + 1 == CW / 32) release(buf ^ 1);
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        const float2 b0 = *reinterpret_cast<const float2*>(bias + 32 * c + 8 * j + 2 * (lane & 3));
+                        const float2 b1 = *reinterpret_cast<const float2*>(bias + 32 * c + 8 * j + 8 + 2 * (lane & 3));
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const float* a = v[hh] + 4 * j;
+                            // matrix `mat`: positions 16 hh + 8 (mat & 1) .., columns 8 (4 c + j + (mat >> 1)) ..
+                            const int n = 8 * (4 * c + j + (mat >> 1)) + mr, piece = 4 * (q & 1) + 2 * hh + (mat & 1);
+                            stmatrix4_trans(tc::smem_u32(half_stage) + (q >> 1) * (CW * 128) + n * 128 + 16 * (piece ^ (n & 7)),
+                                            tc::pack2(a[0] + b0.x, a[1] + b0.y), tc::pack2(a[2] + b0.x, a[3] + b0.y),
+                                            tc::pack2(a[4] + b1.x, a[5] + b1.y), tc::pack2(a[6] + b1.x, a[7] + b1.y));
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < CW / 8; ++j) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 a = unpair(acc[hh][j + (i >> 1)][i & 1]), bb = i < 2 ? b0 : b1;
-                        w[i] = tc::pack2(a.x + bb.x, a.y + bb.y);
+                    for (int i = 0; i < 4; i += 2) {
+                        const float2 a0 = unpair(acc[4 * j + i]), a1 = unpair(acc[4 * j + i + 1]);
+                        const float4 bb = *reinterpret_cast<const float4*>(bias + 8 * j + 2 * i);
+                        w[i] = tc::pack2(a0.x + bb.x, a0.y + bb.y);
+                        w[i + 1] = tc::pack2(a1.x + bb.z, a1.y + bb.w);
                     }
-                    // matrix `mat`: rows 16 hh + 8 (mat & 1) .., columns 8 (j + (mat >> 1)) ..
-                    if (p.channels_first) {
-                        const int n = 8 * (j + (mat >> 1)) + mr, piece = 4 * (q & 1) + 2 * hh + (mat & 1);
-                        stmatrix4_trans(tc::smem_u32(half_stage) + (q >> 1) * (CW * 128) + n * 128 + 16 * (piece ^ (n & 7)), w[0], w[1], w[2], w[3]);
-                    } else {
-                        const int r = 16 * hh + 8 * (mat & 1) + mr, cg = j + (mat >> 1), box = cg / (kBox / 8), c = cg % (kBox / 8);
-                        const int at = kBox == 64 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-                        stmatrix4(tc::smem_u32(stage) + box * (32 * kBox * 2) + r * (kBox * 2) + 16 * at, w[0], w[1], w[2], w[3]);
-                    }
+                    const int box = j / (kBox / 8), c = j % (kBox / 8);
+                    const int at = kBox == 64 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
+                    *reinterpret_cast<uint4*>(stage + box * (32 * kBox * 2) + lane * (kBox * 2) + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             if (p.store == STORE_PLAIN) {
