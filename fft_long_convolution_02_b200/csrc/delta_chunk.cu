@@ -572,6 +572,9 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
     }
 }
 
+// The scans launch while the last CTAs of k_delta_prep drain and wait here for what it wrote.
+__device__ __forceinline__ void after_prep() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // The loading warps of a scanning CTA whose channels start at d0 (cols of them): `put_v` brings V.
 template <int DK, bool FIRST, typename Sm, typename PutV>
 __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, int lane, int h, int64_t b, int64_t len, int d0,
@@ -639,6 +642,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         }
     }
     __syncthreads();
+    after_prep();
     if (warp >= NW) {
         // ------------------------------------------------------------ loaders
         // registers of eight warps: 384 x 168 at launch = 128 x 56 + 256 x 224
@@ -1031,6 +1035,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
         }
     }
     __syncthreads();
+    after_prep();
     if (warp >= kNarrowWarps) {
         const int lt = tid - 32 * kNarrowWarps, cols = min(kNarrowCols, a.dv - d0);
         run_loaders<DK, FIRST>(sm, x, lt, lane, h, b, len, d0, [&](typename Sm::Stage& st, const bf16* p, int n) {
@@ -1277,6 +1282,21 @@ cudaError_t launch_prep(const ChunkArgs& x, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename Kernel>
+cudaError_t launch_after_prep(Kernel kernel, dim3 grid, int threads, size_t bytes, const ChunkArgs& x, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, x);
+}
+
 template <int DK, int NW, bool FIRST>
 cudaError_t launch_scan(const ChunkArgs& x, cudaStream_t s) {
     const size_t bytes = sizeof(ScanSmem<DK, NW>);
@@ -1284,8 +1304,7 @@ cudaError_t launch_scan(const ChunkArgs& x, cudaStream_t s) {
     cudaError_t e = raise_smem(k_delta_scan<DK, NW, FIRST>, bytes, x.dev, raised);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned((x.a.dv + 16 * NW - 1) / (16 * NW)), unsigned(x.a.Hv), unsigned(x.a.B));
-    k_delta_scan<DK, NW, FIRST><<<grid, 32 * NW + kLoaders, bytes, s>>>(x);
-    return cudaGetLastError();
+    return launch_after_prep(k_delta_scan<DK, NW, FIRST>, grid, 32 * NW + kLoaders, bytes, x, s);
 }
 
 template <int DK, bool FIRST>
@@ -1295,8 +1314,7 @@ cudaError_t launch_narrow(const ChunkArgs& x, cudaStream_t s) {
     cudaError_t e = raise_smem(k_delta_scan_narrow<DK, FIRST>, bytes, x.dev, raised);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned((x.a.dv + kNarrowCols - 1) / kNarrowCols), unsigned(x.a.Hv), unsigned(x.a.B));
-    k_delta_scan_narrow<DK, FIRST><<<grid, 32 * kNarrowWarps + kLoaders, bytes, s>>>(x);
-    return cudaGetLastError();
+    return launch_after_prep(k_delta_scan_narrow<DK, FIRST>, grid, 32 * kNarrowWarps + kLoaders, bytes, x, s);
 }
 
 template <int DK, bool FIRST>

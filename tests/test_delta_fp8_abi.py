@@ -31,6 +31,15 @@ def _args(**kw):
     return a
 
 
+def test_packed_struct_is_the_declared_one():
+    """The binding packs the struct from numbers: byte for byte what its fields give."""
+    i3 = ctypes.c_int64 * 3
+    st = [(1, 2, 3), (4, 5, 6), (7, 8, 9), (10, 11, 12), (13, 14, 15), (16, 17, 18)]
+    a = hb.DeltaRule(21, 22, 23, 24, 25, 26, 1, 1, 0.5, 31, 32, 33, 34, 35, 36, *(i3(*x) for x in st), 41, 42, 43)
+    packed = hb._DELTA.pack(21, 22, 23, 24, 25, 26, 1, 1, 0.5, 31, 32, 33, 34, 35, 36, *sum(st, ()), 41, 42, 43)
+    assert packed == bytes(a)
+
+
 @pytest.mark.parametrize("change,want", [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
     (dict(B=0), INVALID), (dict(L=0), INVALID), (dict(dk=0), INVALID), (dict(Hv=0), INVALID), (dict(Hk=0), INVALID),
