@@ -416,7 +416,13 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  *             state before the first).
  *   scale     0 selects dk^-0.5
  *   dtype     storage of q, k, v, o.  The state, g, beta and every sum are fp32.
- *             HYENA_F32 runs token by token in fp32 on the CUDA cores.
+ *             HYENA_F32, and HYENA_BF16 up to 16 tokens, run token by token in
+ *             fp32 on the CUDA cores.  Longer bf16 sequences run in chunks of
+ *             64 tokens on the tensor cores: the state as exact to fp32
+ *             rounding, the outputs through fp16 operands of their bf16
+ *             rounding's size.  There an infinity or NaN among a row's own
+ *             tokens can reach the outputs of up to 63 tokens before it, and
+ *             keys or queries below 1e-18 in norm lose bits.
  *
  * 1 <= dk <= 128, 1 <= dv <= 256, Hv a multiple of Hk, B <= 65535, L <= 2^30,
  * Hv <= 4096.  q, k, v and o may start at any element (alignment of the

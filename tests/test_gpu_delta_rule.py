@@ -351,6 +351,51 @@ def test_long_sequence_sampled():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("dtype,L", [("bf16", 80), ("bf16", 9), ("f32", 20)])
+def test_broadcast_operands(dtype, L):
+    """Keys shared by the batch, one query for all positions and one gate for all heads, as views of stride 0."""
+    c = Case(3, L, 2, 2, 64, 64, dtype)
+    c.k = c.k[:1].expand(3, -1, -1)
+    c.q = c.q[:, :, :1].expand(-1, -1, L)
+    c.g, c.beta = c.g[:, :1].expand(-1, 2, -1), c.beta[:1].expand(3, -1, -1)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("L", [70, 5])
+def test_offsets_beyond_32_bits(L):
+    """Batch rows more than 2^31 elements apart, of the stream and of the output."""
+    import torch
+    c = Case(2, L, 1, 1, 64, 64)
+    far = (1 << 31) + 64
+    buf = torch.empty(far + 4 * 64 * L, dtype=torch.bfloat16, device="cuda")
+    views = [torch.as_strided(buf, (2, 64, L), (far, L, 1), 64 * L * i) for i in range(4)]
+    for v, t in zip(views, (c.q, c.k, c.v)):
+        v.copy_(t)
+    o = torch.full((far + 64 * L,), 0, dtype=torch.bfloat16, device="cuda")
+    c.q, c.k, c.v = views[:3]
+    o2 = torch.as_strided(o, (2, 64, L), (far, L, 1))
+    c.check(*c.run(o2))
+    assert int(torch.count_nonzero(o[64 * L:far])) == 0
+
+
+def test_step_slot_beyond_32_bits():
+    """A pool of more than 2^31 floats: the last state is the one that changes."""
+    import torch
+    n = (1 << 31) // (64 * 64) + 3
+    c = Case(1, 1, 1, 1, 64, 64, "bf16", "last")
+    ro, rs = c.oracle()
+    pool = torch.empty(n, 1, 64, 64, device="cuda")
+    pool[-1] = c.s0[0]
+    pool[2] = 4.0                                         # where the index would land, cut to 32 bits
+    o = torch.empty(1, 64, dtype=torch.bfloat16, device="cuda")
+    hb.hyena_delta_rule_step(c.q[:, :, 0], c.k[:, :, 0], c.v[:, :, 0], c.g[:, :, 0], c.beta[:, :, 0], o, pool, 1, 1,
+                             torch.tensor([n - 1], dtype=torch.int32, device="cuda"), l2norm=True)
+    torch.cuda.synchronize()
+    hb.hyena_kernel_status()
+    assert _rel(_np(o), ro[:, :, 0]) <= OUT("bf16", 64, 1)
+    assert _rel(_np(pool[-1]), rs[0]) <= STATE(64, 1) and (pool[2] == 4.0).all()
+
+
 # ------------------------------------------------------------------------ step
 @pytest.mark.parametrize("B,Hk,Hv,dk,dv", [(1, 1, 1, 128, 128), (3, 2, 4, 64, 96), (2, 1, 3, 100, 40), (5, 1, 1, 7, 33),
                                            (2, 2, 2, 1, 1), (1, 1, 1, 128, 256), (70, 1, 2, 64, 64), (160, 2, 2, 128, 100)])
