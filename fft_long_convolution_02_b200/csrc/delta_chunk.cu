@@ -963,7 +963,7 @@ struct NarrowSmem {
 // An 8 x 8 block of 16-bit numbers transposed across a warp's registers.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
     return r;
 }
 // Two numbers of a 16 x 8 accumulator tile's rows as high and low right operands.
@@ -1092,9 +1092,11 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
         {
             uint32_t r[2][4], w[2][4];
             rows(r[0], w[0], 0);
+            Right y(S[0], ps0.up, ps1.up);
 #pragma unroll
             for (int ks = 0; ks < kTiles; ++ks) {
-                const Right y(S[ks], ps0.up, ps1.up);
+                // the next right operand is made under this one's products
+                const Right next(S[ks + 1 < kTiles ? ks + 1 : ks], ps0.up, ps1.up);
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     const int step = 4 * ks + mt, at = step & 1;
@@ -1103,6 +1105,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
                     mma_f16(O[mt], w[at], y.hi[0], y.hi[1]);
                     mma_f16(X[mt], r[at], y.lo[0], y.lo[1]);
                 }
+                y = next;
             }
         }
         m0 = m1 = 0.0f;
@@ -1124,18 +1127,23 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             O[mt][3] = O[mt][3] * ps1.down * co1;
         }
         const Pow2 pr0(column_max(m0)), pr1(column_max(m1));
-        // U = T R, blocks on and under the diagonal
+        // U = T R, blocks on and under the diagonal (block 0 .. 9: column ks, rows ks .. 3)
+        {
+            const Right y[4] = {{X[0], pr0.up, pr1.up}, {X[1], pr0.up, pr1.up}, {X[2], pr0.up, pr1.up}, {X[3], pr0.up, pr1.up}};
+            constexpr int kCol[11] = {0, 0, 0, 0, 1, 1, 1, 2, 2, 3, 3}, kRow[11] = {0, 1, 2, 3, 1, 2, 3, 2, 3, 3, 3};
+            uint32_t r[2][4], w[2][4];
+            left_mk<8>(r[0], tb, 0, 0, lane);
+            left_mk<8>(w[0], tb + kTile, 0, 0, lane);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const Right y(X[ks], pr0.up, pr1.up);
-#pragma unroll
-            for (int mt = ks; mt < 4; ++mt) {
-                uint32_t r[4], w[4];
-                left_mk<8>(r, tb, mt, ks, lane);
-                left_mk<8>(w, tb + kTile, mt, ks, lane);
-                mma_f16(U[mt], r, y.hi[0], y.hi[1]);
-                mma_f16(U[mt], r, y.lo[0], y.lo[1]);
-                mma_f16(U[mt], w, y.hi[0], y.hi[1]);
+            for (int i = 0; i < 10; ++i) {
+                const int at = i & 1, ks = kCol[i], mt = kRow[i];
+                if (i < 9) {
+                    left_mk<8>(r[at ^ 1], tb, kRow[i + 1], kCol[i + 1], lane);
+                    left_mk<8>(w[at ^ 1], tb + kTile, kRow[i + 1], kCol[i + 1], lane);
+                }
+                mma_f16(U[mt], r[at], y[ks].hi[0], y[ks].hi[1]);
+                mma_f16(U[mt], r[at], y[ks].lo[0], y[ks].lo[1]);
+                mma_f16(U[mt], w[at], y[ks].hi[0], y[ks].hi[1]);
             }
         }
         m0 = m1 = 0.0f;
