@@ -41,8 +41,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // state rows 4 p + 32 j + i (j < J, i < 4), so a lane's k and q come as
 // conflict-free 16-byte reads.  Tokens are staged 32 at a time: q, k, v as
 // fp32 in shared memory, norms and q.k per token by a warp.  The chain per
-// token (two dot products, three shuffles, the update) bounds it: it serves
-// fp32 storage, where every product is fp32.
+// token (two dot products, three shuffles, the update) bounds it, about 0.3 us:
+// it serves fp32 storage, where every product is fp32, and a few tokens.
 constexpr int kSeqT = 32, kSeqCols = 32, kSeqThreads = 256, kSeqRow = 132;
 
 template <typename T, int J>
@@ -362,7 +362,8 @@ bool meets_operand(const Range& r, const hyena_delta_rule_t* p) {
            (p->lengths && r.meets(flat(p->lengths, 4 * p->B)));
 }
 
-// bf16 storage runs in chunks from a few tokens on; below, one launch of the token-by-token kernel is sooner done.
+// bf16 storage runs in chunks from a few tokens on; below, one launch of the token-by-token kernel is sooner done (four
+// heads of 64: 9.4 us at 16 tokens, where the chunked form takes 13; 22.3 against 12.1 us at 64).
 constexpr int64_t kSeqMost = 16;
 bool chunked(int64_t L, int dtype) { return dtype == HYENA_BF16 && L > kSeqMost; }
 

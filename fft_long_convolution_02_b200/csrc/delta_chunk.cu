@@ -188,7 +188,9 @@ __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
 // diagonal by substitution (a thread a column, the columns in registers), then
 // twice the block under two inverses as -T22 (A21 T11).  Its chain of short
 // steps bounds it, so what counts is how many CTAs an SM holds: A and T lie
-// where K and Q were.
+// where K and Q were, five to an SM.  22 ns a chunk (dk = 128, 16384 chunks
+// 359 us; 611 us with three CTAs an SM and 32 x 32 substitutions), 53 % of the
+// issue slots.
 constexpr int kPrepThreads = 128;
 constexpr int kARow = 68;
 
@@ -465,8 +467,14 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
 // so a chunk's chain has no shared-memory round trip and no barrier.  The
 // loaders bring K and Q to fp16 under their powers of two, V as it is, and T, P
 // and the factors as one bulk copy, two chunks deep.
-// mma.sync, not tcgen05: the chain's four dependent products take registers to
-// registers here, and a CTA's 16 x 64 operands are below tcgen05's 128 rows.
+// mma.sync, not tcgen05: the chain's four dependent products go from registers
+// to registers here, where each of tcgen05's would wait for a commit, a read of
+// tensor memory, the split into two parts and a store of it.
+// A chunk of 128 channels takes 11900 cycles for 6400 of products (eight warps,
+// 43 % of the tensor pipe, 38 % of the issue slots), of 64 channels 7100 for
+// 3200: the splits and scalings between the products of an in-order warp bound
+// it, and the registers of the state the number of warps.  256 heads of 64
+// chunks 906 us.
 constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
 constexpr int kORow = 16;                          // elements of a token's row of a warp's outputs
@@ -948,7 +956,9 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
 //   X = K S,  R = V - diag(cx) X,  U = T R,  S = gamma S + K^T (diag(cu) U),  O = diag(co) Q S + P U,
 // and a result becomes the next one's right operand by transposing its 8 x 8
 // blocks in registers.  Every warp reads all of K, Q, T and P as left operands,
-// so shared memory would bound more than four warps an SM.
+// so shared memory would bound more than four warps an SM.  A chunk takes 5100
+// cycles, the warp's and its scheduler's loading warp's issue slots two thirds
+// of them: 24 heads of 128 chunks 350 us (500 us with 16 channels a warp).
 constexpr int kNarrowWarps = 4, kNarrowCols = 8 * kNarrowWarps;
 constexpr int kNarrowVRow = kNarrowCols + 8;       // elements of a token's row of V: eight rows on 32 banks
 
@@ -1329,11 +1339,17 @@ template <int DK, bool FIRST>
 cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
     cudaError_t e = launch_prep<DK, FIRST>(x, s);
     if (e != cudaSuccess) return e;
-    // Narrow CTAs (32 channels) while every one of them has an SM; then four warps of 16 channels, a scheduler each; eight
-    // share them, which pays once half-width CTAs would not all be resident.
-    const int64_t heads = x.a.B * x.a.Hv, ctas = heads * ((x.a.dv + 63) / 64);
-    if (heads * ((x.a.dv + kNarrowCols - 1) / kNarrowCols) <= x.sms) return launch_narrow<DK, FIRST>(x, s);
-    return ctas <= x.sms ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
+    // A chunk takes a CTA of 32, 64 or 128 channels about 5100, 7100 or 11900 cycles (dk = 128): the form whose waves of
+    // CTAs take least.  Measured at L = 1024, dk = dv = 128, us by width: 32 heads 65, 82, 115; 72 heads 128, 107, 133;
+    // 144 heads 246, -, 160.
+    const int64_t heads = x.a.B * x.a.Hv;
+    auto cycles = [&](int width, int64_t each) {
+        const int64_t ctas = heads * ((x.a.dv + width - 1) / width);
+        return (ctas + x.sms - 1) / x.sms * each;
+    };
+    const int64_t narrow = cycles(32, 5100), half = cycles(64, 7100), full = cycles(128, 11900);
+    if (narrow <= half && narrow <= full) return launch_narrow<DK, FIRST>(x, s);
+    return half <= full ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
 }
 
 }  // namespace
