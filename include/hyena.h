@@ -50,7 +50,7 @@
  *    N-D paths is kept as bf16 pairs in the workspace.
  *  - All work is enqueued on `stream` (a cudaStream_t, NULL = legacy default
  *    stream) and is asynchronous: no call synchronises the host.  The
- *    convolution kernels are launched with programmatic stream serialisation:
+ *    convolution kernels and the delta rule's scan are launched with programmatic stream serialisation:
  *    one may begin (build its tables in shared memory) while the kernel before
  *    it on the stream finishes, but reads and writes no global memory before
  *    that kernel has completed, so plain stream order holds for the data.
@@ -433,7 +433,8 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  * workspace: hyena_delta_rule_workspace_bytes() bytes, 16-byte aligned (NULL
  * when that is 0); its contents are undefined after the call, and two calls
  * that may run at the same time need one each.  Asynchronous on `stream`,
- * may be captured into a graph.
+ * may be captured into a graph.  A bounded device wait that runs out is
+ * reported by hyena_kernel_status; the state of that head is NaN then.
  */
 #define HYENA_DELTA_L2NORM 0x1u
 

@@ -61,6 +61,20 @@ def test_delta_rule_refusals(lib, change, want):
     assert lib.hyena_last_error_detail()
 
 
+def test_delta_rule_workspace_refusals(lib):
+    """Chunked sequences want their workspace: its size, alignment and a place of its own."""
+    need = lib.hyena_delta_rule_workspace_bytes(2, 64, 2, 4, 32, 16, hb.HYENA_BF16)
+    assert need > 0
+    assert lib.hyena_delta_rule_workspace_bytes(2, 16, 2, 4, 32, 16, hb.HYENA_BF16) == 0
+    assert lib.hyena_delta_rule_workspace_bytes(2, 64, 2, 4, 32, 16, hb.HYENA_F32) == 0
+    a = ctypes.byref(_args())
+    assert lib.hyena_delta_rule(a, None, 0, None) == 5
+    assert lib.hyena_delta_rule(a, 9 * BIG, need - 1, None) == 5
+    assert lib.hyena_delta_rule(a, 9 * BIG + 8, need, None) == ALIGN
+    for at in (BIG, 2 * BIG, 3 * BIG, 4 * BIG, 5 * BIG, 6 * BIG):
+        assert lib.hyena_delta_rule(a, at, need, None) == INVALID
+
+
 def test_delta_rule_null_struct(lib):
     assert lib.hyena_delta_rule(None, None, 0, None) == INVALID
     assert lib.hyena_delta_rule_step(None, BIG, 4, None, None) == INVALID
