@@ -294,11 +294,24 @@ class DeltaRule(ctypes.Structure):
 _DELTA = struct.Struct("@qq5iIf4x6P18q3P")
 
 
-def _on_device(*tensors) -> int:
+_torch = None
+
+
+def _lazy_torch():
+    """torch, imported by the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _on_device(first, *others) -> int:
     """The kernels run on the current device: its own tensors only (None passes)."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
+    dev = first.get_device()
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
+        raise ValueError(f"tensor on {first.device}, not on the current CUDA device")
+    for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     return dev
@@ -307,8 +320,7 @@ def _on_device(*tensors) -> int:
 def _raw_stream(stream, dev: int) -> int:
     """The stream's handle; of the device's current stream without an object around it."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -326,18 +338,20 @@ def _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, states, three)
     """Shapes checked, tensors and strides packed; (dk, dv) and the struct's
     bytes, with `states` (state_in, state_out, lengths).  three: [B, C, L] and
     [B, Hv, L]; otherwise [B, C] and [B, Hv]."""
-    import torch
+    torch = _torch
     if Hk < 1 or Hv < 1 or q.shape[1] % Hk or v.shape[1] % Hv:
         raise ValueError("the channels of q and k must divide into Hk heads, those of v into Hv")
     dk, dv = q.shape[1] // Hk, v.shape[1] // Hv
     ck, cv, heads = ((B, Hk * dk, L), (B, Hv * dv, L), (B, Hv, L)) if three else ((B, Hk * dk), (B, Hv * dv), (B, Hv))
-    dtype = q.dtype
-    for name, t, c in (("q", q, ck), ("k", k, ck), ("v", v, cv), ("o", o, cv)):
-        if t.shape != c or t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype} {c}, got {t.dtype} {tuple(t.shape)}")
-    for name, t in (("g", g), ("beta", beta)):
-        if t is not None and (t.shape != heads or t.dtype != torch.float32):
-            raise ValueError(f"{name} must be float32 {heads}, got {t.dtype} {tuple(t.shape)}")
+    dtype, f32 = q.dtype, torch.float32
+    code = HYENA_BF16 if dtype is torch.bfloat16 else _dtype_code(q)
+    if (q.shape != ck or k.shape != ck or v.shape != cv or o.shape != cv or k.dtype is not dtype or v.dtype is not dtype
+            or o.dtype is not dtype or g is not None and (g.shape != heads or g.dtype is not f32)
+            or beta is not None and (beta.shape != heads or beta.dtype is not f32)):
+        for name, t, c, d in (("q", q, ck, dtype), ("k", k, ck, dtype), ("v", v, cv, dtype), ("o", o, cv, dtype),
+                              ("g", g, heads, f32), ("beta", beta, heads, f32)):
+            if t is not None and (t.shape != c or t.dtype is not d):
+                raise ValueError(f"{name} must be {d} {c}, got {t.dtype} {tuple(t.shape)}")
     state_in, state_out, lengths = states
     if state_in is not None:
         _plain("state_in", state_in, (B, Hv, dk, dv), torch.float32)
@@ -348,7 +362,7 @@ def _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, states, three)
     last = () if three else (0,)                      # one token: the third stride
     try:
         packed = _DELTA.pack(
-            B, L, Hk, Hv, dk, dv, _dtype_code(q), HYENA_DELTA_L2NORM if l2norm else 0, 0.0 if scale is None else scale,
+            B, L, Hk, Hv, dk, dv, code, HYENA_DELTA_L2NORM if l2norm else 0, 0.0 if scale is None else scale,
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), 0 if g is None else g.data_ptr(),
             0 if beta is None else beta.data_ptr(), *q.stride(), *last, *k.stride(), *last, *v.stride(), *last, *o.stride(),
             *last, *(_NONE3 if g is None else g.stride() + last), *(_NONE3 if beta is None else beta.stride() + last),
@@ -373,7 +387,7 @@ def hyena_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in=None, state
     [B, Hv, L] f32 or None, state_in/state_out: [B, Hv, dk, dv] f32 or None,
     lengths: [B] int32 or None, workspace: uint8 of
     hyena_delta_rule_workspace_bytes(...) or None when that is 0."""
-    import torch
+    torch = _lazy_torch()
     dev = _on_device(q, k, v, g, beta, o, state_in, state_out, lengths, workspace)
     B, _, L = q.shape
     _, _, packed = _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, scale, l2norm, (state_in, state_out, lengths), True)
@@ -386,7 +400,7 @@ def hyena_delta_rule_step(q, k, v, g, beta, o, states, Hk: int, Hv: int, slots=N
     """One token a row: q, k: [B, Hk*dk], v, o: [B, Hv*dv], g, beta: [B, Hv] or
     None, states: [n, Hv, dk, dv] f32 updated in place, slots: [B] int32 (row b
     uses state slots[b], negative: padding) or None (row b uses state b)."""
-    import torch
+    torch = _lazy_torch()
     dev = _on_device(q, k, v, g, beta, o, states, slots)
     B = q.shape[0]
     dk, dv, packed = _delta_args(q, k, v, g, beta, o, B, 1, Hk, Hv, scale, l2norm, _NONE_STATES, False)
@@ -400,7 +414,7 @@ def hyena_delta_rule_step(q, k, v, g, beta, o, states, Hk: int, Hv: int, slots=N
 def hyena_quantize_fp8(x, xq, xs, channels_first: bool = False, stream=None) -> None:
     """x [B, L, K] (or [B, K, L] with channels_first) f32 or bf16 -> xq [B, L, K]
     float8_e4m3fn, xs [B, ceil(K/128), L] f32."""
-    import torch
+    torch = _lazy_torch()
     dev = _on_device(x, xq, xs)
     B, L, K = (x.shape[0], x.shape[2], x.shape[1]) if channels_first else x.shape
     _plain("x", x, x.shape, x.dtype)
@@ -412,7 +426,7 @@ def hyena_quantize_fp8(x, xq, xs, channels_first: bool = False, stream=None) -> 
 
 def hyena_quantize_fp8_weight(W, Wq, Ws, stream=None) -> None:
     """W [N, K] f32 or bf16 -> Wq [N, K] float8_e4m3fn, Ws [ceil(N/128), ceil(K/128)] f32."""
-    import torch
+    torch = _lazy_torch()
     dev = _on_device(W, Wq, Ws)
     N, K = W.shape
     _plain("W", W, (N, K), W.dtype)
@@ -425,7 +439,7 @@ def hyena_quantize_fp8_weight(W, Wq, Ws, stream=None) -> None:
 def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stream=None) -> None:
     """xq [B, L, K], Wq [N, K] float8_e4m3fn with their scales, bias [N] f32 or
     None -> out bf16 [B, L, N], or [B, N, L] with channels_first."""
-    import torch
+    torch = _lazy_torch()
     dev = _on_device(xq, xs, Wq, Ws, bias, out)
     B, L, K = xq.shape
     N = Wq.shape[0]
