@@ -346,7 +346,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 bool shapes_ok(int64_t B, int64_t L, int Hk, int Hv, int dk, int dv) {
     return B >= 1 && B <= 65535 && L >= 1 && L <= (int64_t(1) << 30) && Hk >= 1 && Hv >= Hk && Hv <= 4096 &&
-           Hv % Hk == 0 && dk >= 1 && dk <= kDeltaMaxDk && dv >= 1 && dv <= kDeltaMaxDv;
+           Hv % Hk == 0 && dk >= 1 && dk <= kDeltaMaxDk && dv >= 1 && dv <= kDeltaMaxDv && B * Hv * L <= (int64_t(1) << 40);
 }
 
 // Whether a range meets any operand of *p (its strides and sizes checked).
@@ -374,7 +374,7 @@ hyena_status_t prepare_delta(const hyena_delta_rule_t* p, DeltaArgs* a) {
         return fail(HYENA_ERR_INVALID_ARG, "B, L, Hk, Hv, dk and dv must be >= 1");
     if (!shapes_ok(p->B, p->L, p->Hk, p->Hv, p->dk, p->dv))
         return fail(HYENA_ERR_UNSUPPORTED_SHAPE,
-                    "needs B <= 65535, L <= 2^30, Hv a multiple of Hk up to 4096, dk <= 128 and dv <= 256");
+                    "needs B <= 65535, L <= 2^30, B Hv L <= 2^40, Hv a multiple of Hk up to 4096, dk <= 128 and dv <= 256");
     if (p->dtype != HYENA_F32 && p->dtype != HYENA_BF16)
         return fail(HYENA_ERR_INVALID_ARG, "dtype must be HYENA_F32 or HYENA_BF16");
     if (p->flags & ~HYENA_DELTA_L2NORM) return fail(HYENA_ERR_INVALID_ARG, "unknown flag bits");

@@ -424,7 +424,7 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  *             tokens can reach the outputs of up to 63 tokens before it, and
  *             keys or queries below 1e-18 in norm lose bits.
  *
- * 1 <= dk <= 128, 1 <= dv <= 256, Hv a multiple of Hk, B <= 65535, L <= 2^30,
+ * 1 <= dk <= 128, 1 <= dv <= 256, Hv a multiple of Hk, B <= 65535, L <= 2^30, B Hv L <= 2^40,
  * Hv <= 4096.  q, k, v and o may start at any element (alignment of the
  * dtype); states are 16-byte aligned, g, beta and lengths 4-byte.  Input
  * strides are >= 0, those of o must give every element a place of its own, and
@@ -513,7 +513,8 @@ hyena_status_t hyena_quantize_fp8_weight(const void* W, void* Wq, float* Ws, int
  *   out     bf16, [B, N, L] (channels_first = 1: what hyena_shortconv and the
  *           mixers read) or [B, L, N] (channels_first = 0)
  * Products and sums are fp32, the result is rounded once (to nearest even).
- * K a multiple of 16, L and N any, B <= 65535, B * L <= 2^31 - 1, N and K <= 2^20; xq, Wq, out
+ * K a multiple of 16, L and N any, B <= 65535, B * L <= 2^31 - 1, N and K <= 2^20, out of fewer than
+ * 2^31 tiles of 128 x 64; xq, Wq, out
  * 16-byte aligned, xs, Ws, bias 4-byte; out may not overlap an input.  A
  * bounded device wait that runs out is reported by hyena_kernel_status.
  */

@@ -45,6 +45,7 @@ def test_packed_struct_is_the_declared_one():
     (dict(B=0), INVALID), (dict(L=0), INVALID), (dict(dk=0), INVALID), (dict(Hv=0), INVALID), (dict(Hk=0), INVALID),
     (dict(B=65536), SHAPE), (dict(L=(1 << 30) + 1), SHAPE), (dict(Hv=3), SHAPE), (dict(dk=129), SHAPE),
     (dict(dv=257), SHAPE), (dict(Hk=8), SHAPE), (dict(Hv=8192), SHAPE),
+    (dict(B=65535, L=1 << 30), SHAPE),
     (dict(dtype=2), INVALID), (dict(flags=2), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID),
     (dict(q=BIG + 1), ALIGN), (dict(o=4 * BIG + 1), ALIGN), (dict(g=5 * BIG + 2), ALIGN), (dict(beta=6 * BIG + 2), ALIGN),
@@ -95,6 +96,7 @@ def test_delta_step_refusals(lib, change, states, n, slots, want):
 
 def test_delta_workspace_of_bad_arguments(lib):
     f = lib.hyena_delta_rule_workspace_bytes
+    assert f(65535, 1 << 30, 1, 4096, 64, 64, 1) == 0     # would not fit 64 bits of bytes
     assert f(0, 64, 1, 1, 64, 64, 1) == 0 and f(1, 64, 2, 3, 64, 64, 1) == 0 and f(1, 64, 1, 1, 64, 64, 5) == 0
 
 
