@@ -199,6 +199,38 @@ def test_decays(dtype, decay):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_growing_gates(dtype):
+    """Gates of either sign: a chunk's products may grow the state too (up to e^3 here)."""
+    c = Case(1, 130, 1, 2, 64, 64, dtype)
+    c.g[:] = (c.g + 0.2) * 0.25
+    c.g[:, :, 20:40] = 0.15
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("Hk,Hv", [(2, 4), (1, 3), (1, 4), (1, 8), (2, 10)])
+@pytest.mark.parametrize("layout", ["first", "last"])
+def test_shared_key_heads_of_many_chunks(Hk, Hv, layout):
+    """Chunks enough for the value heads of a key head to be taken together, by twos, threes and fours."""
+    B, L = 12, 64 * 16 * 5 + 9
+    c = Case(B, L, Hk, Hv, 16, 16, layout=layout, lengths=[L, 100] + [int(L * b / B) for b in range(2, B)])
+    import torch
+    o, s1 = c.run()
+    d = Case(B, L, Hv, Hv, 16, 16, layout=layout)          # the same with the key heads written out
+    r = Hv // Hk
+    rep = lambda x: x.reshape(B, Hk, 16, L).repeat_interleave(r, 1).reshape(B, Hv * 16, L)
+    d.q, d.k, d.v, d.g, d.beta, d.s0, d.lengths = rep(c.q), rep(c.k), c.v, c.g, c.beta, c.s0, c.lengths
+    o2, s2 = d.run()
+    for b in range(B):
+        n = int(c.lengths[b])
+        assert torch.equal(o[b, :, :n], o2[b, :, :n])
+    assert torch.equal(s1, s2)
+    few = [1]                                              # and against the oracle where that is quick
+    ro, rs = dr.delta_rule(*(_np(t[few]) for t in (c.q, c.k, c.v, c.g, c.beta)), Hk, Hv, _np(c.s0[few]), [100], l2norm=True)
+    assert _rel(_np(o[1, :, :100]), ro[0, :, :100]) <= OUT("bf16", 16, 100)
+    assert _rel(_np(s1[few]), rs) <= STATE(16, 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_reset_by_minus_infinity(dtype):
     """g = -inf empties the state: what came before is forgotten exactly, inside a chunk and on its border."""
     import torch
