@@ -212,7 +212,6 @@ struct PrepSmem {
     alignas(16) float W[32][36];
     alignas(16) float gh[kGroup][C], gl[kGroup][C], beta[kGroup][C];   // gh + gl: sums of the log2 decays
     alignas(16) float rk[C], rq[C], kn[C], qn[C];                  // norms' inverses (rq times the scale), norms
-    float grow[kGroup];                            // at least every e^{G_i - G_j}, j <= i: 1 for decays
 };
 
 // W = A[r0 + N ..][c0 ..] T[c0 ..][c0 ..], then T[r0 ..][c0 ..] = -T[r0 ..][r0 ..] W, for the N x N block under the
@@ -300,10 +299,6 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             v[j] = double(d) * 1.4426950408889634;
             sm.beta[warp][t] = t < n ? (a.beta ? a.beta[b * a.bs.sb + h * a.bs.sc + (t0 + t) * a.bs.st] : 1.0f) : 0.0f;
         }
-        float up = fmaxf(float(v[0]), 0.0f) + fmaxf(float(v[1]), 0.0f);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) up += __shfl_xor_sync(0xffffffffu, up, d);
-        if (lane == 0) sm.grow[warp] = exp2f(up);
         double s = v[0] + v[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -368,10 +363,6 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         }
     }
     __syncthreads();                               // norms; and K, Q have been read
-    // the largest of the scaled keys: with it and the query's norm a row of P is bounded
-    float kmax = fmaxf(sm.rk[lane] * sm.kn[lane], sm.rk[lane + 32] * sm.kn[lane + 32]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, d));
 #pragma unroll 1
     for (int hh = 0; hh < group; ++hh) {
     const float *gh = sm.gh[hh], *gl = sm.gl[hh], *beta = sm.beta[hh];
@@ -392,14 +383,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         const int r0 = 16 * warp + g, r1 = r0 + 8;
         const float h0 = gh[r0], h1 = gh[r1], l0 = gl[r0], l1 = gl[r1];
         const float a0 = beta[r0] * sm.rk[r0], a1 = beta[r1] * sm.rk[r1];
-        const float most = kmax * sm.grow[hh];
-        const Pow2 p0(fabsf(sm.rq[r0]) * sm.qn[r0] * most), p1(fabsf(sm.rq[r1]) * sm.qn[r1] * most);
         const float q0 = sm.rq[r0], q1 = sm.rq[r1];
-        if (t4 == 0) {
-            f->cp[r0] = p0.down;
-            f->cp[r1] = p1.down;
-        }
-        uint8_t* P2 = blob + 2 * kTile + 4 * t4;
+        float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
             if (nt > 2 * warp + 1) break;          // what lies right of the diagonal's blocks is not read
@@ -413,12 +398,31 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             for (int j = 0; j < 4; ++j) {
                 const int r = j < 2 ? r0 : r1, cc = c + (j & 1);
                 av[j] = cc < r ? (j < 2 ? a0 : a1) * d[j] * ka[nt][j] : 0.0f;
-                pv[j] = cc <= r ? d[j] * (j < 2 ? q0 : q1) * qa[nt][j] * (j < 2 ? p0.up : p1.up) : 0.0f;
+                pv[j] = cc <= r ? d[j] * (j < 2 ? q0 : q1) * qa[nt][j] : 0.0f;
             }
+            m0 = fmaxf(m0, fmaxf(fabsf(pv[0]), fabsf(pv[1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(pv[2]), fabsf(pv[3])));
             *reinterpret_cast<float2*>(&sm.A[r0][c]) = make_float2(av[0], av[1]);
             *reinterpret_cast<float2*>(&sm.A[r1][c]) = make_float2(av[2], av[3]);
-            *reinterpret_cast<uint32_t*>(P2 + piece<8>(r0, nt)) = pack_h(pv[0], pv[1]);
-            *reinterpret_cast<uint32_t*>(P2 + piece<8>(r1, nt)) = pack_h(pv[2], pv[3]);
+            // P waits where T comes later, each thread's for itself
+            *reinterpret_cast<float2*>(&sm.T[r0][c]) = make_float2(pv[0], pv[1]);
+            *reinterpret_cast<float2*>(&sm.T[r1][c]) = make_float2(pv[2], pv[3]);
+        }
+        // A row of P goes to fp16 under its own largest element: a bound from the norms and gates (one product of it may be
+        // large where the row's elements are not, with gates of either sign or a later large key) would cost it all its bits.
+        const Pow2 p0(quad_max(m0)), p1(quad_max(m1));
+        if (t4 == 0) {
+            f->cp[r0] = p0.down;
+            f->cp[r1] = p1.down;
+        }
+        uint8_t* P2 = blob + 2 * kTile + 4 * t4;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt > 2 * warp + 1) break;
+            const int c = 8 * nt + 2 * t4;
+            const float2 v0 = *reinterpret_cast<const float2*>(&sm.T[r0][c]), v1 = *reinterpret_cast<const float2*>(&sm.T[r1][c]);
+            *reinterpret_cast<uint32_t*>(P2 + piece<8>(r0, nt)) = pack_h(v0.x * p0.up, v0.y * p0.up);
+            *reinterpret_cast<uint32_t*>(P2 + piece<8>(r1, nt)) = pack_h(v1.x * p1.up, v1.y * p1.up);
         }
     }
     __syncthreads();
