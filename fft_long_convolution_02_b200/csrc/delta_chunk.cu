@@ -13,12 +13,14 @@
 // registers.
 //
 // Precision.  The state and what feeds it are held to fp32: K and Q are exact in
-// fp16 once a power of two brings a row's largest element to [2^13, 2^14)
-// (8 significant bits; what falls below 2^-37 of the row's largest is lost), and
-// S, T, V - .. and U go into the products as two fp16 parts each, 22 bits, under
-// such a power of two for each row (the low parts stay normal numbers down to
-// 2^-27 of the row's largest).  Sums are fp32.  The outputs are bf16, so on
-// their way S, P and U are one fp16 part each (11 bits).
+// fp16 once a power of two brings a row's norm to [2^14, 2^15) (8 significant
+// bits; what falls below 2^-39 of the norm is lost), and S, T, V - .. and U go
+// into the products as two fp16 parts each under such a power of two for the
+// largest element of each row: 22 bits of what is above 2^-17 of the largest,
+// below that 2^-39 of the largest (the low part is subnormal then).  Sums are
+// fp32.  The outputs are bf16, so on their way S, P and U are one fp16 part each:
+// 11 bits of what is above 2^-28 of a row's largest, below that the same 2^-39.
+// A chunk where that would not do is taken token by token ("far apart" below).
 // e^{G_i - G_j} comes from sums held as two floats: their difference loses
 // nothing behind a strong decay.
 #include <cuda_bf16.h>
@@ -40,6 +42,19 @@ using bf16 = __nv_bfloat16;
 
 constexpr int C = 64;                              // tokens of a chunk
 
+// Bounds that tell a chunk whose magnitudes lie too far apart (see the scans).  u, r: a channel's largest write and
+// residual; n: its largest entry of U diag(cu); s: of the state before the chunk.
+struct alignas(16) Reach {
+    float w, k;                                    // T's largest times what its row's write leaves in the state; the largest key
+    int first;                                     // the first token that writes (C: none)
+    __device__ __forceinline__ bool end(float u, float r, float n, float s, float gamma) const {
+        return fmaxf(n * 0x1p14f, gamma * s) < fmaxf(r * w, u * k);
+    }
+    __device__ __forceinline__ bool start(float u_first, float u, float s, float gamma) const {
+        return u_first < u * 0x1p-28f && fminf(gamma, 1.0f) * s < u * k;
+    }
+};
+
 // What k_delta_prep leaves for a chunk of a value head: T's two parts and P as
 // fp16 images of the scan's shared memory, and the factors of its 64 tokens.
 struct Factors {
@@ -49,7 +64,9 @@ struct Factors {
     float co[C];                                   // (Q S) row of the scaled Q to the output
     float cp[C], ct[C];                            // rows of the stored P and T to P and T
     float gamma;                                   // e^{G_63}
-    float pad[63];
+    float pad0[3];
+    Reach reach;
+    float pad[56];
 };
 constexpr uint32_t kTile = C * C * 2;              // bytes of a 64 x 64 fp16 image
 constexpr uint32_t kBlob = 3 * kTile + uint32_t(sizeof(Factors));
@@ -105,12 +122,12 @@ __device__ __forceinline__ void left_km(uint32_t (&r)[4], uint32_t tile, int m16
     ldsm4t(r, tile + piece<PIECES>(16 * k16 + 8 * (m >> 1) + (lane & 7), 2 * m16 + (m & 1)));
 }
 
-// The power of two that brings a largest magnitude m to [2^13, 2^14), and its
+// The power of two that brings a largest magnitude m to [2^14, 2^15), and its
 // inverse; both normal numbers whatever m is.
 struct Pow2 {
     float up, down;
     __device__ __forceinline__ explicit Pow2(float m) {
-        int e = 267 - int(__float_as_uint(m) >> 23);
+        int e = 268 - int(__float_as_uint(m) >> 23);
         e = max(1, min(253, e));
         up = __uint_as_float(uint32_t(e) << 23);
         down = __uint_as_float(uint32_t(254 - e) << 23);
@@ -212,6 +229,10 @@ struct PrepSmem {
     alignas(16) float W[32][36];
     alignas(16) float gh[kGroup][C], gl[kGroup][C], beta[kGroup][C];   // gh + gl: sums of the log2 decays
     alignas(16) float rk[C], rq[C], kn[C], qn[C];                  // norms' inverses (rq times the scale), norms
+    float left[C];                                 // what a token's write leaves at the chunk's end, times its key
+    float kmost[2];                                // largest of the scaled keys, by halves of the chunk
+    int first[2];                                  // first token that writes, by halves (C: none)
+    float strict[kGroup];                          // 2^-24, or 2^-18 where a gate grows the state
 };
 
 // W = A[r0 + N ..][c0 ..] T[c0 ..][c0 ..], then T[r0 ..][c0 ..] = -T[r0 ..][r0 ..] W, for the N x N block under the
@@ -299,6 +320,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             v[j] = double(d) * 1.4426950408889634;
             sm.beta[warp][t] = t < n ? (a.beta ? a.beta[b * a.bs.sb + h * a.bs.sc + (t0 + t) * a.bs.st] : 1.0f) : 0.0f;
         }
+        const bool grows = __any_sync(0xffffffffu, v[0] > 0.0 || v[1] > 0.0);
+        if (lane == 0) sm.strict[warp] = grows ? 0x1p-18f : 0x1p-24f;
         double s = v[0] + v[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -377,7 +400,17 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         f->cx[t] = into * sm.rk[t] * pk.down;
         f->cu[t] = out * sm.rk[t] * pk.down;
         f->co[t] = into * sm.rq[t] * pq.down;
-        if (t == 0) f->gamma = exp2f(gh[C - 1] + gl[C - 1]);
+        if (t == 0) {
+            f->gamma = exp2f(gh[C - 1] + gl[C - 1]);
+            f->reach.w = 0.0f;
+        }
+        sm.left[t] = out * sm.rk[t] * sm.kn[t];
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(sm.rk[t] * sm.kn[t]));      // not negative
+        const unsigned writes = __ballot_sync(0xffffffffu, beta[t] != 0.0f && sm.kn[t] > 1e-18f);
+        if (lane == 0) {
+            sm.kmost[warp] = __uint_as_float(most);
+            sm.first[warp] = writes ? 32 * warp + __ffs(int(writes)) - 1 : C;
+        }
     }
     {
         const int r0 = 16 * warp + g, r1 = r0 + 8;
@@ -464,6 +497,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const Pow2 p(m);
         if (c0 == 0) f->ct[r] = p.down;
+        // not negative, so ordered as their bits; NaN above all, and then no comparison holds
+        const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(m * sm.left[r])));
+        if (lane == 0) atomicMax(reinterpret_cast<uint32_t*>(&f->reach.w), __float_as_uint(__uint_as_float(w) * sm.strict[hh]));
+        if (tid == 0) {
+            f->reach.k = fmaxf(sm.kmost[0], sm.kmost[1]) * 0x1p-28f;
+            f->reach.first = min(sm.first[0], sm.first[1]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (c0 + 8 * i > (r | 15)) break;
@@ -499,6 +539,27 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
 constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
 constexpr int kORow = 16;                          // elements of a token's row of a warp's outputs
+
+// Chunks whose magnitudes lie too far apart for the products.  A channel's R and
+// U, and a row of T and P, go in under one power of two each, whose fp16 numbers
+// end at 2^-39 of the largest.  A value far above its neighbours (one that a write
+// strength of 0 masks, too), a large state that a gate empties halfway, keys of
+// very unequal size, or gates that grow the state would thus cost the other
+// tokens their outputs, or the state its bits.  Such a chunk is told from a
+// channel's largest numbers before its state changes, and the warp takes it token
+// by token in fp32: 64 tokens take 36 us with the narrow scan (2.4 us by products,
+// dk = 64), 75 us with 64 channels a CTA (5.3, dk = 128).
+//   state    what remains of it and of the writes below 2^-24 of the largest
+//            residual times the largest of T (2^-18 where gates grow the state):
+//            above that the errors of U, 2^-39 of those, stay within 2^-16 of the
+//            state (measured: 2^-22 up to ratios of 2^18, 2^-20 at 2^20, 2^-16 at 2^24);
+//   outputs  the writes, key and decay with them, below 2^-28 of the largest write
+//            and key at the end of the chunk; the chunk's first write, or two
+//            neighbouring writes, below 2^-28 of the largest.
+// A single write far below the others is left alone: their terms make the output,
+// and chance brings one in 10^4 chunks.  Looking for all this costs 1 % (4 x 8192
+// x 6 heads 432 -> 436 us) to 3 % (16 x 4096 x 16 heads 1195 -> 1230 us).
+__device__ __forceinline__ bool below(float write, float largest) { return write != 0.0f && write < largest * 0x1p-28f; }
 
 template <int DK, int VR, int VC>
 struct ScanStage {
@@ -652,6 +713,126 @@ __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, 
     // the last copies land before the CTA may end: the scanning warps wait for every stage
 }
 
+// One element of a tile of 16-bit numbers [token][channel], or (FIRST) [channel][token].
+template <int DK, bool FIRST>
+__device__ __forceinline__ __half tile_at(const uint8_t* tile, int t, int ch) {
+    const uint32_t at = FIRST ? piece<8>(ch, t >> 3) + 2u * uint32_t(t & 7) : piece<DK / 8>(t, ch >> 3) + 2u * uint32_t(ch & 7);
+    return *reinterpret_cast<const __half*>(tile + at);
+}
+
+// n tokens of a chunk one by one, from the definition.  The state as the scans hold it, two channels a thread: WIDE
+// S^T tiles (element i: channel i / 2, row 8 j + 2 t4 + i % 2), else S tiles (channel i % 2, row 16 j + g + 8 (i / 2)).
+// v, o: this thread's first channel at the chunk's first token, in shared memory, with the strides of channel and token;
+// gate, beta: the chunk's, or nullptr.
+struct Tokens {
+    const uint8_t *k, *q;
+    const float *kmul, *qmul, *gate, *beta;
+    int64_t gate_step, beta_step;
+    const bf16* v;
+    bf16* o;
+    int v_channel, v_token, o_channel, o_token;
+    int n, l2norm;
+    float scale;
+};
+template <int DK, bool FIRST, bool WIDE, int J>
+__device__ __forceinline__ void chunk_by_token(float (&S)[J][4], const Tokens& x) {
+    const int lane = int(threadIdx.x) & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    auto row = [&](int j, int e) { return WIDE ? 8 * j + 2 * t4 + e : 16 * j + g + 8 * e; };      // e: one of a tile's two
+    auto whole_sum = [&](float v) {                // over the lanes that share this one's channels
+#pragma unroll
+        for (int d = WIDE ? 1 : 4; d < (WIDE ? 4 : 32); d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    };
+    auto at = [](int c, int e) { return WIDE ? 2 * c + e : 2 * e + c; };                          // S[j][at(channel, e)]
+    // the gates of tokens `lane` and lane + 32
+    float al[2], be[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = lane + 32 * i;
+        al[i] = x.gate && t < x.n ? expf(x.gate[t * x.gate_step]) : 1.0f;
+        be[i] = x.beta && t < x.n ? x.beta[t * x.beta_step] : 1.0f;
+    }
+#pragma unroll 1
+    for (int t = 0; t < x.n; ++t) {
+        __half2 k[J], q[J];
+        float k2 = 0.0f, q2 = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            k[j] = __halves2half2(tile_at<DK, FIRST>(x.k, t, row(j, 0)), tile_at<DK, FIRST>(x.k, t, row(j, 1)));
+            q[j] = __halves2half2(tile_at<DK, FIRST>(x.q, t, row(j, 0)), tile_at<DK, FIRST>(x.q, t, row(j, 1)));
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float2 kk = __half22float2(k[j]), qq = __half22float2(q[j]);
+            k2 = fmaf(kk.x, kk.x, fmaf(kk.y, kk.y, k2));
+            q2 = fmaf(qq.x, qq.x, fmaf(qq.y, qq.y, q2));
+            x0 = fmaf(S[j][at(0, 0)], kk.x, fmaf(S[j][at(0, 1)], kk.y, x0));
+            x1 = fmaf(S[j][at(1, 0)], kk.x, fmaf(S[j][at(1, 1)], kk.y, x1));
+        }
+        // the tiles hold K and Q times their rows' powers of two
+        const float dk = 1.0f / x.kmul[t], dq = 1.0f / x.qmul[t];
+        k2 = whole_sum(k2) * dk * dk;
+        q2 = whole_sum(q2) * dq * dq;
+        const float rk = (x.l2norm ? 1.0f / sqrtf(k2 + kDeltaNormEps) : 1.0f) * dk;
+        const float rq = (x.l2norm ? 1.0f / sqrtf(q2 + kDeltaNormEps) : 1.0f) * x.scale * dq;
+        const float a = __shfl_sync(0xffffffffu, t < 32 ? al[0] : al[1], t & 31), b = __shfl_sync(0xffffffffu, t < 32 ? be[0] : be[1], t & 31);
+        const float v0 = __bfloat162float(x.v[t * x.v_token]), v1 = __bfloat162float(x.v[x.v_channel + t * x.v_token]);
+        const float u0 = b * (v0 - a * (whole_sum(x0) * rk)) * rk;
+        const float u1 = b * (v1 - a * (whole_sum(x1) * rk)) * rk;
+        float y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float2 kk = __half22float2(k[j]), qq = __half22float2(q[j]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float &s0 = S[j][at(c, 0)], &s1 = S[j][at(c, 1)], &y = c ? y1 : y0;
+                s0 = fmaf(kk.x, c ? u1 : u0, a * s0);
+                s1 = fmaf(kk.y, c ? u1 : u0, a * s1);
+                y = fmaf(s0, qq.x, fmaf(s1, qq.y, y));
+            }
+        }
+        y0 = whole_sum(y0) * rq;
+        y1 = whole_sum(y1) * rq;
+        if ((WIDE ? t4 : g) == 0) {                // one of the lanes that share these channels
+            x.o[t * x.o_token] = __float2bfloat16_rn(y0);
+            x.o[x.o_channel + t * x.o_token] = __float2bfloat16_rn(y1);
+        }
+    }
+}
+template <int J>
+__device__ __forceinline__ void copy_state(float (&to)[J][4], const float (&from)[J][4]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[j][i] = from[j][i];
+}
+template <int DK, bool FIRST, int J>
+__device__ __noinline__ void chunk_by_token_apart(float (&S)[J][4], const Tokens& x) {
+    float own[J][4];                               // registers again
+    copy_state(own, S);
+    chunk_by_token<DK, FIRST, true>(own, x);
+    copy_state(S, own);
+}
+// The same for a scan's state in registers.  The wide scan calls it, which leaves its own registers alone (16 x 4096 x 16
+// heads 1229 us, inlined 1243); in the narrow one it is inlined (4 x 8192 x 6 heads 436 us, called 446).
+template <int DK, bool FIRST, bool WIDE, int J>
+__device__ __forceinline__ void state_by_token(float (&S)[J][4], const uint8_t* k, const uint8_t* q, const Factors& f,
+                                               const DeltaArgs& a, int64_t b, int h, int64_t t0, int n, const bf16* v, int v_channel,
+                                               int v_token, bf16* o, int o_channel, int o_token) {
+    const Tokens x{k, q, f.kmul, f.qmul, a.g ? a.g + b * a.gs.sb + h * a.gs.sc + t0 * a.gs.st : nullptr,
+                   a.beta ? a.beta + b * a.bs.sb + h * a.bs.sc + t0 * a.bs.st : nullptr, a.gs.st, a.bs.st, v, o,
+                   v_channel, v_token, o_channel, o_token, n, a.l2norm, a.scale};
+    if constexpr (WIDE) {
+        float copy[J][4];
+        copy_state(copy, S);
+        chunk_by_token_apart<DK, FIRST>(copy, x);
+        copy_state(S, copy);
+    } else {
+        chunk_by_token<DK, FIRST, false>(S, x);
+    }
+}
+
 template <int DK, int NW, bool FIRST>
 __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs x) {
     using Sm = ScanSmem<DK, NW>;
@@ -706,6 +887,8 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             for (int j = 0; j < DK / 8; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
             break;
         }
+        const int64_t t0 = int64_t(ch) * C;
+        const int n = int(min(int64_t(C), len - t0));
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
         const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
         float m0 = 0.0f, m1 = 0.0f;
@@ -714,7 +897,8 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             m0 = fmaxf(m0, fmaxf(fabsf(S[j][0]), fabsf(S[j][1])));
             m1 = fmaxf(m1, fmaxf(fabsf(S[j][2]), fabsf(S[j][3])));
         }
-        const Pow2 ps0(quad_max(m0)), ps1(quad_max(m1));
+        const float s0 = quad_max(m0), s1 = quad_max(m1);
+        const Pow2 ps0(s0), ps1(s1);
         float X[8][4], O[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -771,7 +955,8 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             O[nt][2] = O[nt][2] * ps1.down * co.x;
             O[nt][3] = O[nt][3] * ps1.down * co.y;
         }
-        const Pow2 pr0(quad_max(m0)), pr1(quad_max(m1));
+        const float r0 = quad_max(m0), r1 = quad_max(m1);
+        const Pow2 pr0(r0), pr1(r1);
         // U^T = R^T T^T, tiles on and right of the diagonal
         float U[8][4];
 #pragma unroll
@@ -800,6 +985,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             }
         }
         m0 = m1 = 0.0f;
+        float z0 = INFINITY, z1 = z0;              // the smallest write: of the first tokens each, then of two the larger
         float n0 = 0.0f, n1 = 0.0f;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
@@ -809,8 +995,11 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             U[nt][1] = U[nt][1] * pr0.down * ct.y;
             U[nt][2] = U[nt][2] * pr1.down * ct.x;
             U[nt][3] = U[nt][3] * pr1.down * ct.y;
-            m0 = fmaxf(m0, fmaxf(fabsf(U[nt][0]), fabsf(U[nt][1])));
-            m1 = fmaxf(m1, fmaxf(fabsf(U[nt][2]), fabsf(U[nt][3])));
+            const float p0 = fmaxf(fabsf(U[nt][0]), fabsf(U[nt][1])), p1 = fmaxf(fabsf(U[nt][2]), fabsf(U[nt][3]));
+            m0 = fmaxf(m0, p0);
+            m1 = fmaxf(m1, p1);
+            z0 = fminf(z0, nt == 0 ? fminf(fabsf(U[nt][0]), fabsf(U[nt][1])) : p0);
+            z1 = fminf(z1, nt == 0 ? fminf(fabsf(U[nt][2]), fabsf(U[nt][3])) : p1);
             X[nt][0] = U[nt][0] * cu.x;
             X[nt][1] = U[nt][1] * cu.y;
             X[nt][2] = U[nt][2] * cu.x;
@@ -818,102 +1007,132 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             n0 = fmaxf(n0, fmaxf(fabsf(X[nt][0]), fabsf(X[nt][1])));
             n1 = fmaxf(n1, fmaxf(fabsf(X[nt][2]), fabsf(X[nt][3])));
         }
-        const Pow2 pu0(quad_max(m0)), pu1(quad_max(m1)), pw0(quad_max(n0)), pw1(quad_max(n1));
-        // S^T = gamma S^T + (U diag(cu))^T K
-        uint32_t hi[4][4], lo[4][4];
+        const float u0 = quad_max(m0), u1 = quad_max(m1), w0 = quad_max(n0), w1 = quad_max(n1), gamma = f.gamma;
+        const Reach reach = f.reach;
+        const bool end = reach.end(u0, r0, w0, s0, gamma) || reach.end(u1, r1, w1, s1, gamma);
+        if (n < C) {                               // behind the end nothing is written
+            z0 = z1 = INFINITY;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+            for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                split_h(X[2 * ks + j][0] * pw0.up, X[2 * ks + j][1] * pw0.up, hi[ks][2 * j], lo[ks][2 * j]);
-                split_h(X[2 * ks + j][2] * pw1.up, X[2 * ks + j][3] * pw1.up, hi[ks][2 * j + 1], lo[ks][2 * j + 1]);
-            }
-        const float gamma = f.gamma;
-        auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
-            const int ks = step % 4, nt = 4 * (step / 4);
-            if constexpr (FIRST) {
-                right_nk<P>(r, tk, ks, nt, lane);
-                right_nk<P>(w, tk, ks, nt + 2, lane);
-            } else {
-                right_kn<P>(r, tk, ks, nt, lane);
-                right_kn<P>(w, tk, ks, nt + 2, lane);
-            }
-        };
-        {
-            uint32_t r[2][4], w[2][4];
-            keys_t(r[0], w[0], 0);
-            float D[4][4];
+                for (int i = 0; i < 2; ++i)
+                    if (8 * nt + 2 * t4 + i < n) {
+                        z0 = fminf(z0, fabsf(U[nt][i]));
+                        z1 = fminf(z1, fabsf(U[nt][i + 2]));
+                    }
+        }
+        bool apart = __any_sync(0xffffffffu, end || z0 < u0 * 0x1p-28f || z1 < u1 * 0x1p-28f);
+        if (__builtin_expect(apart, 0)) {          // or tokens that write nothing, or one write by chance?
+            bool far = end;
 #pragma unroll
-            for (int step = 0; step < DK / 8; ++step) {
-                const int ks = step % 4, nt = 4 * (step / 4), at = step & 1;
-                if (step + 1 < DK / 8) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
-                if (ks == 0) {
+            for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) D[i][j] = 0.0f;
+                for (int c = 0; c < 2; ++c) {
+                    const float a0 = fabsf(U[nt][2 * c]), a1 = fabsf(U[nt][2 * c + 1]), u = c ? u1 : u0, s = c ? s1 : s0;
+                    far = far || below(fmaxf(a0, a1), u) || (reach.first == 8 * nt + 2 * t4 && reach.start(a0, u, s, gamma)) ||
+                          (reach.first == 8 * nt + 2 * t4 + 1 && reach.start(a1, u, s, gamma));
                 }
-                mma_f16(D[0], hi[ks], r[at][0], r[at][1]);
-                mma_f16(D[1], hi[ks], r[at][2], r[at][3]);
-                mma_f16(D[2], hi[ks], w[at][0], w[at][1]);
-                mma_f16(D[3], hi[ks], w[at][2], w[at][3]);
-                mma_f16(D[0], lo[ks], r[at][0], r[at][1]);
-                mma_f16(D[1], lo[ks], r[at][2], r[at][3]);
-                mma_f16(D[2], lo[ks], w[at][0], w[at][1]);
-                mma_f16(D[3], lo[ks], w[at][2], w[at][3]);
-                if (ks == 3) {
+            apart = __any_sync(0xffffffffu, far);
+        }
+        if (__builtin_expect(apart, 0)) {
+            state_by_token<DK, FIRST, true>(S, st.k, st.q, f, a, b, h, t0, n, &st.v[16 * warp + g][0], 8 * kVRow, 1,
+                                            so + g * (FIRST ? kVRow : 1), 8 * (FIRST ? kVRow : 1), FIRST ? 1 : kORow);
+        } else {
+            const Pow2 pu0(u0), pu1(u1), pw0(w0), pw1(w1);
+            uint32_t hi[4][4], lo[4][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        S[nt + i][0] = fmaf(gamma, S[nt + i][0], D[i][0] * pw0.down);
-                        S[nt + i][1] = fmaf(gamma, S[nt + i][1], D[i][1] * pw0.down);
-                        S[nt + i][2] = fmaf(gamma, S[nt + i][2], D[i][2] * pw1.down);
-                        S[nt + i][3] = fmaf(gamma, S[nt + i][3], D[i][3] * pw1.down);
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    split_h(X[2 * ks + j][0] * pw0.up, X[2 * ks + j][1] * pw0.up, hi[ks][2 * j], lo[ks][2 * j]);
+                    split_h(X[2 * ks + j][2] * pw1.up, X[2 * ks + j][3] * pw1.up, hi[ks][2 * j + 1], lo[ks][2 * j + 1]);
+                }
+            // S^T = gamma S^T + (U diag(cu))^T K
+            auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+                const int ks = step % 4, nt = 4 * (step / 4);
+                if constexpr (FIRST) {
+                    right_nk<P>(r, tk, ks, nt, lane);
+                    right_nk<P>(w, tk, ks, nt + 2, lane);
+                } else {
+                    right_kn<P>(r, tk, ks, nt, lane);
+                    right_kn<P>(w, tk, ks, nt + 2, lane);
+                }
+            };
+            {
+                uint32_t r[2][4], w[2][4];
+                keys_t(r[0], w[0], 0);
+                float D[4][4];
+#pragma unroll
+                for (int step = 0; step < DK / 8; ++step) {
+                    const int ks = step % 4, nt = 4 * (step / 4), at = step & 1;
+                    if (step + 1 < DK / 8) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
+                    if (ks == 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) D[i][j] = 0.0f;
+                    }
+                    mma_f16(D[0], hi[ks], r[at][0], r[at][1]);
+                    mma_f16(D[1], hi[ks], r[at][2], r[at][3]);
+                    mma_f16(D[2], hi[ks], w[at][0], w[at][1]);
+                    mma_f16(D[3], hi[ks], w[at][2], w[at][3]);
+                    mma_f16(D[0], lo[ks], r[at][0], r[at][1]);
+                    mma_f16(D[1], lo[ks], r[at][2], r[at][3]);
+                    mma_f16(D[2], lo[ks], w[at][0], w[at][1]);
+                    mma_f16(D[3], lo[ks], w[at][2], w[at][3]);
+                    if (ks == 3) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            S[nt + i][0] = fmaf(gamma, S[nt + i][0], D[i][0] * pw0.down);
+                            S[nt + i][1] = fmaf(gamma, S[nt + i][1], D[i][1] * pw0.down);
+                            S[nt + i][2] = fmaf(gamma, S[nt + i][2], D[i][2] * pw1.down);
+                            S[nt + i][3] = fmaf(gamma, S[nt + i][3], D[i][3] * pw1.down);
+                        }
                     }
                 }
             }
-        }
-        // O^T += U^T P^T
+            // O^T += U^T P^T
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
+                for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t u[4];
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t u[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                u[2 * j] = pack_h(U[2 * ks + j][0] * pu0.up, U[2 * ks + j][1] * pu0.up);
-                u[2 * j + 1] = pack_h(U[2 * ks + j][2] * pu1.up, U[2 * ks + j][3] * pu1.up);
+                for (int j = 0; j < 2; ++j) {
+                    u[2 * j] = pack_h(U[2 * ks + j][0] * pu0.up, U[2 * ks + j][1] * pu0.up);
+                    u[2 * j + 1] = pack_h(U[2 * ks + j][2] * pu1.up, U[2 * ks + j][3] * pu1.up);
+                }
+#pragma unroll
+                for (int nt = 2 * ks; nt < 8; nt += 2) {
+                    uint32_t r[4];
+                    right_nk<8>(r, tb + 2 * kTile, ks, nt, lane);
+                    mma_f16(X[nt], u, r[0], r[1]);
+                    mma_f16(X[nt + 1], u, r[2], r[3]);
+                }
             }
+            // out through shared memory: whole rows leave
 #pragma unroll
-            for (int nt = 2 * ks; nt < 8; nt += 2) {
-                uint32_t r[4];
-                right_nk<8>(r, tb + 2 * kTile, ks, nt, lane);
-                mma_f16(X[nt], u, r[0], r[1]);
-                mma_f16(X[nt + 1], u, r[2], r[3]);
-            }
-        }
-        // out through shared memory: whole rows leave
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            const int t = 8 * nt + 2 * t4;
-            const float2 cp = *reinterpret_cast<const float2*>(&f.cp[t]);
-            const __nv_bfloat162 y0 = __floats2bfloat162_rn(fmaf(X[nt][0] * pu0.down, cp.x, O[nt][0]), fmaf(X[nt][1] * pu0.down, cp.y, O[nt][1]));
-            const __nv_bfloat162 y1 = __floats2bfloat162_rn(fmaf(X[nt][2] * pu1.down, cp.x, O[nt][2]), fmaf(X[nt][3] * pu1.down, cp.y, O[nt][3]));
-            if constexpr (FIRST) {
-                *reinterpret_cast<__nv_bfloat162*>(so + g * kVRow + t) = y0;
-                *reinterpret_cast<__nv_bfloat162*>(so + (g + 8) * kVRow + t) = y1;
-            } else {
-                so[t * kORow + g] = y0.x;
-                so[(t + 1) * kORow + g] = y0.y;
-                so[t * kORow + g + 8] = y1.x;
-                so[(t + 1) * kORow + g + 8] = y1.y;
+            for (int nt = 0; nt < 8; ++nt) {
+                const int t = 8 * nt + 2 * t4;
+                const float2 cp = *reinterpret_cast<const float2*>(&f.cp[t]);
+                const __nv_bfloat162 y0 = __floats2bfloat162_rn(fmaf(X[nt][0] * pu0.down, cp.x, O[nt][0]), fmaf(X[nt][1] * pu0.down, cp.y, O[nt][1]));
+                const __nv_bfloat162 y1 = __floats2bfloat162_rn(fmaf(X[nt][2] * pu1.down, cp.x, O[nt][2]), fmaf(X[nt][3] * pu1.down, cp.y, O[nt][3]));
+                if constexpr (FIRST) {
+                    *reinterpret_cast<__nv_bfloat162*>(so + g * kVRow + t) = y0;
+                    *reinterpret_cast<__nv_bfloat162*>(so + (g + 8) * kVRow + t) = y1;
+                } else {
+                    so[t * kORow + g] = y0.x;
+                    so[(t + 1) * kORow + g] = y0.y;
+                    so[t * kORow + g + 8] = y1.x;
+                    so[(t + 1) * kORow + g + 8] = y1.y;
+                }
             }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
-        const int64_t t0 = int64_t(ch) * C;
-        const int n = int(min(int64_t(C), len - t0)), cols = min(16, a.dv - dw);
+        const int cols = min(16, a.dv - dw);
         bf16* oc = ob + t0 * a.os.st;
         if (x.vec_o && n == C && cols == 16) {
             // whole rows of 16 bytes, all in flight
@@ -1096,6 +1315,8 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             for (int j = 0; j < kTiles; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
             break;
         }
+        const int64_t t0 = int64_t(ch) * C;
+        const int n = int(min(int64_t(C), len - t0));
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
         const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
         float m0 = 0.0f, m1 = 0.0f;
@@ -1104,7 +1325,8 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             m0 = fmaxf(m0, fmaxf(fabsf(S[j][0]), fabsf(S[j][2])));
             m1 = fmaxf(m1, fmaxf(fabsf(S[j][1]), fabsf(S[j][3])));
         }
-        const Pow2 ps0(column_max(m0)), ps1(column_max(m1));
+        const float s0 = column_max(m0), s1 = column_max(m1);
+        const Pow2 ps0(s0), ps1(s1);
         float X[4][4], O[4][4], U[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1157,7 +1379,8 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             O[mt][2] = O[mt][2] * ps0.down * co1;
             O[mt][3] = O[mt][3] * ps1.down * co1;
         }
-        const Pow2 pr0(column_max(m0)), pr1(column_max(m1));
+        const float r0 = column_max(m0), r1 = column_max(m1);
+        const Pow2 pr0(r0), pr1(r1);
         // U = T R, blocks on and under the diagonal (block 0 .. 9: column ks, rows ks .. 3)
         {
             const Right y[4] = {{X[0], pr0.up, pr1.up}, {X[1], pr0.up, pr1.up}, {X[2], pr0.up, pr1.up}, {X[3], pr0.up, pr1.up}};
@@ -1178,6 +1401,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             }
         }
         m0 = m1 = 0.0f;
+        float z0 = INFINITY, z1 = z0;              // the smallest write
         float n0 = 0.0f, n1 = 0.0f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
@@ -1189,6 +1413,8 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             U[mt][3] = U[mt][3] * pr1.down * ct1;
             m0 = fmaxf(m0, fmaxf(fabsf(U[mt][0]), fabsf(U[mt][2])));
             m1 = fmaxf(m1, fmaxf(fabsf(U[mt][1]), fabsf(U[mt][3])));
+            z0 = fminf(z0, fminf(fabsf(U[mt][0]), fabsf(U[mt][2])));
+            z1 = fminf(z1, fminf(fabsf(U[mt][1]), fabsf(U[mt][3])));
             X[mt][0] = U[mt][0] * cu0;
             X[mt][1] = U[mt][1] * cu0;
             X[mt][2] = U[mt][2] * cu1;
@@ -1196,81 +1422,112 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             n0 = fmaxf(n0, fmaxf(fabsf(X[mt][0]), fabsf(X[mt][2])));
             n1 = fmaxf(n1, fmaxf(fabsf(X[mt][1]), fabsf(X[mt][3])));
         }
-        const Pow2 pu0(column_max(m0)), pu1(column_max(m1)), pw0(column_max(n0)), pw1(column_max(n1));
-        // S = gamma S + K^T (diag(cu) U), two tiles of key channels at a time
-        {
-            const Right y[4] = {{X[0], pw0.up, pw1.up}, {X[1], pw0.up, pw1.up}, {X[2], pw0.up, pw1.up}, {X[3], pw0.up, pw1.up}};
-            auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
-                const int i = 2 * (step / 4), ks = step % 4;
-                if constexpr (FIRST) {
-                    left_mk<P>(r, tk, i, ks, lane);
-                    left_mk<P>(w, tk, i + 1, ks, lane);
-                } else {
-                    left_km<P>(r, tk, i, ks, lane);
-                    left_km<P>(w, tk, i + 1, ks, lane);
+        const float u0 = column_max(m0), u1 = column_max(m1), w0 = column_max(n0), w1 = column_max(n1), gamma = f.gamma;
+        const Reach reach = f.reach;
+        const bool end = reach.end(u0, r0, w0, s0, gamma) || reach.end(u1, r1, w1, s1, gamma);
+        if (n < C) {                               // behind the end nothing is written
+            z0 = z1 = INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (16 * mt + g + 8 * i < n) {
+                        z0 = fminf(z0, fabsf(U[mt][2 * i]));
+                        z1 = fminf(z1, fabsf(U[mt][2 * i + 1]));
+                    }
+        }
+        bool apart = __any_sync(0xffffffffu, end || z0 < u0 * 0x1p-28f || z1 < u1 * 0x1p-28f);
+        if (__builtin_expect(apart, 0)) {          // or tokens that write nothing, or one write by chance?
+            bool far = end;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a0 = fabsf(U[mt][i]), u = (i & 1) ? u1 : u0, s = (i & 1) ? s1 : s0;
+                    const float a1 = __shfl_xor_sync(0xffffffffu, a0, 4);
+                    far = far || below(fmaxf(a0, a1), u) ||
+                          (reach.first == 16 * mt + g + 8 * (i >> 1) && reach.start(a0, u, s, gamma));
                 }
-            };
-            const float gamma = f.gamma;
-            uint32_t r[2][4], w[2][4];
-            keys_t(r[0], w[0], 0);
-            float D[4][4];
+            apart = __any_sync(0xffffffffu, far);
+        }
+        if (__builtin_expect(apart, 0)) {
+            state_by_token<DK, FIRST, false>(S, st.k, st.q, f, a, b, h, t0, n, &st.v[0][8 * warp + 2 * t4], 1, kNarrowVRow,
+                                             so + 2 * t4 * (FIRST ? kVRow : 1), FIRST ? kVRow : 1, FIRST ? 1 : 8);
+        } else {
+            const Pow2 pu0(u0), pu1(u1), pw0(w0), pw1(w1);
+            const Right yw[4] = {{X[0], pw0.up, pw1.up}, {X[1], pw0.up, pw1.up}, {X[2], pw0.up, pw1.up}, {X[3], pw0.up, pw1.up}};
+            // S = gamma S + K^T (diag(cu) U), two tiles of key channels at a time
+            {
+                auto keys_t = [&](uint32_t (&r)[4], uint32_t (&w)[4], int step) {
+                    const int i = 2 * (step / 4), ks = step % 4;
+                    if constexpr (FIRST) {
+                        left_mk<P>(r, tk, i, ks, lane);
+                        left_mk<P>(w, tk, i + 1, ks, lane);
+                    } else {
+                        left_km<P>(r, tk, i, ks, lane);
+                        left_km<P>(w, tk, i + 1, ks, lane);
+                    }
+                };
+                uint32_t r[2][4], w[2][4];
+                keys_t(r[0], w[0], 0);
+                float D[4][4];
 #pragma unroll
-            for (int step = 0; step < 2 * kTiles; ++step) {
-                const int i = 2 * (step / 4), ks = step % 4, at = step & 1;
-                if (step + 1 < 2 * kTiles) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
-                if (ks == 0) {
+                for (int step = 0; step < 2 * kTiles; ++step) {
+                    const int i = 2 * (step / 4), ks = step % 4, at = step & 1;
+                    if (step + 1 < 2 * kTiles) keys_t(r[at ^ 1], w[at ^ 1], step + 1);
+                    if (ks == 0) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) D[0][j] = D[1][j] = D[2][j] = D[3][j] = 0.0f;
-                }
-                mma_f16(D[0], r[at], y[ks].hi[0], y[ks].hi[1]);
-                mma_f16(D[1], w[at], y[ks].hi[0], y[ks].hi[1]);
-                mma_f16(D[2], r[at], y[ks].lo[0], y[ks].lo[1]);
-                mma_f16(D[3], w[at], y[ks].lo[0], y[ks].lo[1]);
-                if (ks == 3) {
+                        for (int j = 0; j < 4; ++j) D[0][j] = D[1][j] = D[2][j] = D[3][j] = 0.0f;
+                    }
+                    mma_f16(D[0], r[at], yw[ks].hi[0], yw[ks].hi[1]);
+                    mma_f16(D[1], w[at], yw[ks].hi[0], yw[ks].hi[1]);
+                    mma_f16(D[2], r[at], yw[ks].lo[0], yw[ks].lo[1]);
+                    mma_f16(D[3], w[at], yw[ks].lo[0], yw[ks].lo[1]);
+                    if (ks == 3) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float down = (j & 1) ? pw1.down : pw0.down;
-                        S[i][j] = fmaf(gamma, S[i][j], (D[0][j] + D[2][j]) * down);
-                        S[i + 1][j] = fmaf(gamma, S[i + 1][j], (D[1][j] + D[3][j]) * down);
+                        for (int j = 0; j < 4; ++j) {
+                            const float down = (j & 1) ? pw1.down : pw0.down;
+                            S[i][j] = fmaf(gamma, S[i][j], (D[0][j] + D[2][j]) * down);
+                            S[i + 1][j] = fmaf(gamma, S[i + 1][j], (D[1][j] + D[3][j]) * down);
+                        }
                     }
                 }
             }
-        }
-        // O += P U
+            // O += P U
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
+                for (int j = 0; j < 4; ++j) X[i][j] = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t u0 = transposed(pack_h(U[ks][0] * pu0.up, U[ks][1] * pu1.up));
-            const uint32_t u1 = transposed(pack_h(U[ks][2] * pu0.up, U[ks][3] * pu1.up));
+            for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t u0 = transposed(pack_h(U[ks][0] * pu0.up, U[ks][1] * pu1.up));
+                const uint32_t u1 = transposed(pack_h(U[ks][2] * pu0.up, U[ks][3] * pu1.up));
 #pragma unroll
-            for (int mt = ks; mt < 4; ++mt) {
-                uint32_t r[4];
-                left_mk<8>(r, tb + 2 * kTile, mt, ks, lane);
-                mma_f16(X[mt], r, u0, u1);
+                for (int mt = ks; mt < 4; ++mt) {
+                    uint32_t r[4];
+                    left_mk<8>(r, tb + 2 * kTile, mt, ks, lane);
+                    mma_f16(X[mt], r, u0, u1);
+                }
             }
-        }
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            const int t = 16 * mt + g;
-            const float cp0 = f.cp[t], cp1 = f.cp[t + 8];
-            const uint32_t y0 = tc::pack2(fmaf(X[mt][0] * pu0.down, cp0, O[mt][0]), fmaf(X[mt][1] * pu1.down, cp0, O[mt][1]));
-            const uint32_t y1 = tc::pack2(fmaf(X[mt][2] * pu0.down, cp1, O[mt][2]), fmaf(X[mt][3] * pu1.down, cp1, O[mt][3]));
-            if constexpr (FIRST) {
-                // rows are channels: the blocks transposed
-                *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 2 * t4) = transposed(y0);
-                *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 8 + 2 * t4) = transposed(y1);
-            } else {
-                *reinterpret_cast<uint32_t*>(so + t * 8 + 2 * t4) = y0;
-                *reinterpret_cast<uint32_t*>(so + (t + 8) * 8 + 2 * t4) = y1;
+            for (int mt = 0; mt < 4; ++mt) {
+                const int t = 16 * mt + g;
+                const float cp0 = f.cp[t], cp1 = f.cp[t + 8];
+                const uint32_t y0 = tc::pack2(fmaf(X[mt][0] * pu0.down, cp0, O[mt][0]), fmaf(X[mt][1] * pu1.down, cp0, O[mt][1]));
+                const uint32_t y1 = tc::pack2(fmaf(X[mt][2] * pu0.down, cp1, O[mt][2]), fmaf(X[mt][3] * pu1.down, cp1, O[mt][3]));
+                if constexpr (FIRST) {
+                    // rows are channels: the blocks transposed
+                    *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 2 * t4) = transposed(y0);
+                    *reinterpret_cast<uint32_t*>(so + g * kVRow + 16 * mt + 8 + 2 * t4) = transposed(y1);
+                } else {
+                    *reinterpret_cast<uint32_t*>(so + t * 8 + 2 * t4) = y0;
+                    *reinterpret_cast<uint32_t*>(so + (t + 8) * 8 + 2 * t4) = y1;
+                }
             }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
-        const int64_t t0 = int64_t(ch) * C;
-        const int n = int(min(int64_t(C), len - t0)), cols = min(8, a.dv - dw);
+        const int cols = min(8, a.dv - dw);
         bf16* oc = ob + t0 * a.os.st;
         if (x.vec_o && n == C && cols == 8) {
 #pragma unroll

@@ -418,11 +418,21 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  *   dtype     storage of q, k, v, o.  The state, g, beta and every sum are fp32.
  *             HYENA_F32, and HYENA_BF16 up to 16 tokens, run token by token in
  *             fp32 on the CUDA cores.  Longer bf16 sequences run in chunks of
- *             64 tokens on the tensor cores: the state as exact to fp32
- *             rounding, the outputs through fp16 operands of their bf16
- *             rounding's size.  There an infinity or NaN among a row's own
+ *             64 tokens on the tensor cores.  There the products with the
+ *             state take 22 bits of it, relative to the largest element of a
+ *             value channel's column, so the state comes out within fp32
+ *             rounding of that; the outputs' terms are rounded to 11 bits each
+ *             (scale q.S before the chunk, and the chunk's own writes), which
+ *             is a bf16 rounding of the output unless the terms cancel.  Where
+ *             values, keys or states lie so far apart within a chunk that other
+ *             tokens' outputs or the state would lose more than that, the
+ *             chunk runs token by token instead, some 15 times as long.  A
+ *             channel that gates shrink by 2^18 to 2^24 within a chunk keeps 2^-20
+ *             to 2^-16 of itself.  An infinity or NaN among a row's own
  *             tokens can reach the outputs of up to 63 tokens before it, and
- *             keys or queries below 1e-18 in norm lose bits.
+ *             keys or queries below 1e-18 in norm lose bits.  In all forms the
+ *             square of a key's or query's norm is an fp32 number: norms above
+ *             1.8e19 are outside it.
  *
  * 1 <= dk <= 128, 1 <= dv <= 256, Hv a multiple of Hk, B <= 65535, L <= 2^30, B Hv L <= 2^40,
  * Hv <= 4096.  q, k, v and o may start at any element (alignment of the
