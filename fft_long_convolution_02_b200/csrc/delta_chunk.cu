@@ -557,8 +557,8 @@ constexpr int kORow = 16;                          // elements of a token's row 
 //            and key at the end of the chunk; the chunk's first write, or two
 //            neighbouring writes, below 2^-28 of the largest.
 // A single write far below the others is left alone: their terms make the output,
-// and chance brings one in 10^4 chunks.  Looking for all this costs 1 % (4 x 8192
-// x 6 heads 432 -> 436 us) to 3 % (16 x 4096 x 16 heads 1195 -> 1230 us).
+// and chance brings one in 10^4 chunks.  Looking for all this costs 1 % (16 x 4096
+// x 16 heads 1195 -> 1204 us) to 2 % (4 x 8192 x 6 heads 433 -> 442 us).
 __device__ __forceinline__ bool below(float write, float largest) { return write != 0.0f && write < largest * 0x1p-28f; }
 
 template <int DK, int VR, int VC>
@@ -662,15 +662,16 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
     }
 }
 
-// The scans launch while the last CTAs of k_delta_prep drain and wait here for what it wrote.
+// The scans launch while the last CTAs of k_delta_prep drain and wait here for what it wrote; nothing in global memory is
+// read or written before.
 __device__ __forceinline__ void after_prep() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // The loading warps of a scanning CTA whose channels start at d0 (cols of them): `put_v` brings V.
 template <int DK, bool FIRST, typename Sm, typename PutV>
-__device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, int lane, int h, int64_t b, int64_t len, int d0,
+__device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, int lane, int h, int64_t b, int len, int d0,
                                             PutV put_v) {
     const DeltaArgs& a = x.a;
-    const int chunks = int((len + C - 1) / C);
+    const int chunks = (len + C - 1) / C;
     const int kh = h / (a.Hv / a.Hk);
     const bf16* kp = static_cast<const bf16*>(a.k) + b * a.ks.sb + int64_t(kh) * a.dk * a.ks.sc;
     const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qs.sb + int64_t(kh) * a.dk * a.qs.sc;
@@ -691,7 +692,7 @@ __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, 
                          : "memory");
         }
         const int64_t t0 = int64_t(ch) * C;
-        const int n = int(min(int64_t(C), len - t0));
+        const int n = min(C, len - ch * C);
         load_tile<DK, FIRST>(st.k, kp + t0 * a.ks.st, a.ks, a.dk, n, x.vec_k, lt);
         load_tile<DK, FIRST>(st.q, qp + t0 * a.qs.st, a.qs, a.dk, n, x.vec_q, lt);
         const Factors* f = reinterpret_cast<const Factors*>(blob + 3 * kTile);
@@ -815,7 +816,7 @@ __device__ __noinline__ void chunk_by_token_apart(float (&S)[J][4], const Tokens
     copy_state(S, own);
 }
 // The same for a scan's state in registers.  The wide scan calls it, which leaves its own registers alone (16 x 4096 x 16
-// heads 1229 us, inlined 1243); in the narrow one it is inlined (4 x 8192 x 6 heads 436 us, called 446).
+// heads 1229 us, inlined 1243); in the narrow one it is inlined (4 x 8192 x 6 heads 434 us, called 446).
 template <int DK, bool FIRST, bool WIDE, int J>
 __device__ __forceinline__ void state_by_token(float (&S)[J][4], const uint8_t* k, const uint8_t* q, const Factors& f,
                                                const DeltaArgs& a, int64_t b, int h, int64_t t0, int n, const bf16* v, int v_channel,
@@ -843,8 +844,6 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
     const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int h = int(blockIdx.y), d0 = int(blockIdx.x) * 16 * NW;
     const int64_t b = blockIdx.z;
-    const int64_t len = length_of(a, b);
-    const int chunks = int((len + C - 1) / C);
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&sm.full[s], kLoaders + 1);
@@ -853,6 +852,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
     }
     __syncthreads();
     after_prep();
+    const int len = int(length_of(a, b)), chunks = (len + C - 1) / C;      // L <= 2^30
     if (warp >= NW) {
         // ------------------------------------------------------------ loaders
         // registers of eight warps: 384 x 168 at launch = 128 x 56 + 256 x 224
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             break;
         }
         const int64_t t0 = int64_t(ch) * C;
-        const int n = int(min(int64_t(C), len - t0));
+        const int n = min(C, len - ch * C);
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
         const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
         float m0 = 0.0f, m1 = 0.0f;
@@ -1276,8 +1276,6 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
     const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int h = int(blockIdx.y), d0 = int(blockIdx.x) * kNarrowCols;
     const int64_t b = blockIdx.z;
-    const int64_t len = length_of(a, b);
-    const int chunks = int((len + C - 1) / C);
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&sm.full[s], kLoaders + 1);
@@ -1286,6 +1284,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
     }
     __syncthreads();
     after_prep();
+    const int len = int(length_of(a, b)), chunks = (len + C - 1) / C;      // L <= 2^30
     if (warp >= kNarrowWarps) {
         const int lt = tid - 32 * kNarrowWarps, cols = min(kNarrowCols, a.dv - d0);
         run_loaders<DK, FIRST>(sm, x, lt, lane, h, b, len, d0, [&](typename Sm::Stage& st, const bf16* p, int n) {
@@ -1316,7 +1315,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             break;
         }
         const int64_t t0 = int64_t(ch) * C;
-        const int n = int(min(int64_t(C), len - t0));
+        const int n = min(C, len - ch * C);
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
         const Factors& f = *reinterpret_cast<const Factors*>(st.blob + 3 * kTile);
         float m0 = 0.0f, m1 = 0.0f;
