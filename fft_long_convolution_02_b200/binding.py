@@ -29,7 +29,7 @@ EXPORTS = ["hyena_version", "hyena_status_string", "hyena_last_error_detail", "h
            "hyena_debug_conv_tc", "hyena_debug_conv_cluster", "hyena_debug_conv_2d_tc", "hyena_debug_conv_2dc_tc", "hyena_gated_fftconv_ex", "hyena_kernel_status", "hyena_in_proj",
            "hyena_out_proj", "hyena_implicit_filter_workspace_bytes", "hyena_filter_spectrum_implicit",
            "hyena_delta_rule_workspace_bytes", "hyena_delta_rule", "hyena_delta_rule_step", "hyena_quantize_fp8",
-           "hyena_quantize_fp8_weight", "hyena_proj_fp8"]
+           "hyena_quantize_fp8_weight", "hyena_proj_fp8", "hyena_debug_delta_rule"]
 
 _lock = threading.Lock()
 _lib = None
@@ -115,6 +115,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.hyena_delta_rule_workspace_bytes.argtypes = [i64, i64] + [ctypes.c_int] * 5
         lib.hyena_delta_rule.restype = ctypes.c_int
         lib.hyena_delta_rule.argtypes = [vp, vp, sz, vp]
+        lib.hyena_debug_delta_rule.restype = ctypes.c_int
+        lib.hyena_debug_delta_rule.argtypes = [vp, vp, sz, ctypes.c_uint64, i64, vp]
         lib.hyena_delta_rule_step.restype = ctypes.c_int
         lib.hyena_delta_rule_step.argtypes = [vp, vp, i64, vp, vp]
         lib.hyena_quantize_fp8.restype = ctypes.c_int
@@ -542,3 +544,14 @@ def hyena_debug_conv_cluster(u, y, spectrum, sc_w, sc_bias, B: int, C: int, orde
                                            spectrum.numel() * spectrum.element_size(), _ptr(sc_w), _ptr(sc_bias), B,
                                            C, order, _ptr(workspace), ws_bytes, int(wait_budget_ns),
                                            1 if issue_mma else 0, _stream(stream)))
+
+
+def hyena_debug_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in, state_out, workspace, wait_budget_ns: int,
+                           hold_chunk: int = -1, l2norm: bool = False, stream=None) -> None:
+    """The same test hook for the scans of hyena_delta_rule: the stage of chunk hold_chunk (-1: none) is never freed."""
+    _lazy_torch()
+    dev = _on_device(q, k, v, g, beta, o, state_in, state_out, workspace)
+    B, _, L = q.shape
+    _, _, packed = _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, None, l2norm, (state_in, state_out, None), True)
+    _check(load().hyena_debug_delta_rule(packed, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         int(wait_budget_ns), hold_chunk, _raw_stream(stream, dev)))

@@ -468,13 +468,11 @@ extern "C" size_t hyena_delta_rule_workspace_bytes(int64_t B, int64_t L, int Hk,
     return delta_chunk_workspace(B, L, Hv);
 }
 
-extern "C" hyena_status_t hyena_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
-                                           void* stream) {
-    DeltaArgs a;
-    hyena_status_t st = prepare_delta(p, &a);
-    if (st != HYENA_OK) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!chunked(p->L, p->dtype)) return done(launch_delta_seq(a, p->dtype, s), "delta rule");
+namespace {
+
+// The chunked form: its workspace checked, launched.
+hyena_status_t run_chunked(const hyena_delta_rule_t* p, const DeltaArgs& a, void* workspace, size_t workspace_bytes,
+                           uint64_t budget_ns, int64_t hold, cudaStream_t s) {
     const size_t need = delta_chunk_workspace(p->B, p->L, p->Hv);
     if (!workspace || workspace_bytes < need)
         return fail(HYENA_ERR_WORKSPACE_TOO_SMALL, "workspace must hold at least " + std::to_string(need) + " bytes");
@@ -485,7 +483,30 @@ extern "C" hyena_status_t hyena_delta_rule(const hyena_delta_rule_t* p, void* wo
     uint32_t* status = nullptr;
     cudaError_t e = kernel_status_word(&status);
     if (e != cudaSuccess) return done(e, "kernel status word");
-    return done(launch_delta_chunk(a, workspace, status, s), "delta rule");
+    return done(launch_delta_chunk(a, workspace, status, budget_ns, hold, s), "delta rule");
+}
+
+}  // namespace
+
+extern "C" hyena_status_t hyena_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+    DeltaArgs a;
+    hyena_status_t st = prepare_delta(p, &a);
+    if (st != HYENA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!chunked(p->L, p->dtype)) return done(launch_delta_seq(a, p->dtype, s), "delta rule");
+    return run_chunked(p, a, workspace, workspace_bytes, kDefaultWaitBudgetNs, -1, s);
+}
+
+extern "C" hyena_status_t hyena_debug_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
+                                                 uint64_t wait_budget_ns, int64_t hold_chunk, void* stream) {
+    DeltaArgs a;
+    hyena_status_t st = prepare_delta(p, &a);
+    if (st != HYENA_OK) return st;
+    if (!chunked(p->L, p->dtype))
+        return fail(HYENA_ERR_UNSUPPORTED_SHAPE, "only the chunked form (bf16, more than " + std::to_string(kSeqMost) + " tokens) waits");
+    if (wait_budget_ns == 0) return fail(HYENA_ERR_INVALID_ARG, "wait_budget_ns must be > 0");
+    return run_chunked(p, a, workspace, workspace_bytes, wait_budget_ns, hold_chunk, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" hyena_status_t hyena_delta_rule_step(const hyena_delta_rule_t* p, float* states, int64_t n_states,

@@ -33,7 +33,9 @@ struct DeltaArgs {
 cudaError_t launch_delta_seq(const DeltaArgs& a, int dtype, cudaStream_t s);
 // In chunks of 64 tokens (delta_chunk.cu): bf16 storage, any strides, with a workspace of delta_chunk_workspace().
 size_t delta_chunk_workspace(int64_t B, int64_t L, int Hv);
-cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, cudaStream_t s);
+// The scans' waits give up after budget_ns; `hold` (a test's) is the chunk whose stage is never freed, -1 for none.
+cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, uint64_t budget_ns, int64_t hold,
+                               cudaStream_t s);
 // One token, states in place (delta.cu).
 cudaError_t launch_delta_step(const DeltaArgs& a, int dtype, float* states, int64_t n_states, const int32_t* slots,
                               uint32_t* status, cudaStream_t s);

@@ -190,6 +190,7 @@ struct ChunkArgs {
     int vec_k, vec_q, vec_v, vec_o;                // rows may be read (written) 16 bytes at a time
     int group;                                     // value heads of a k_delta_prep CTA, all of one key head
     uint64_t budget_ns;
+    int hold;                                      // test hook: the chunk whose stage is never freed (-1: none)
     uint32_t* status;
     int dev, sms;
 };
@@ -666,6 +667,11 @@ __device__ __forceinline__ void load_values(bf16 (&v)[16 * NW][kVRow], const bf1
 // read or written before.
 __device__ __forceinline__ void after_prep() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
+// A warp that gives up: the copies of the chunks [from, to) that may be in flight land first.
+__device__ __forceinline__ void landed(uint64_t* full, int from, int to, uint64_t budget_ns) {
+    for (int c = max(from, 0); c < to; ++c) tc::mbar_wait(&full[c & 1], uint32_t(c >> 1) & 1u, budget_ns);
+}
+
 // The loading warps of a scanning CTA whose channels start at d0 (cols of them): `put_v` brings V.
 template <int DK, bool FIRST, typename Sm, typename PutV>
 __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, int lane, int h, int64_t b, int len, int d0,
@@ -682,6 +688,7 @@ __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, 
         auto& st = sm.st[s];
         if (!tc::mbar_wait(&sm.empty[s], (uint32_t(ch >> 1) & 1u) ^ 1u, x.budget_ns)) {
             if (lane == 0) report_status(x.status, kStatusTimeout);
+            landed(sm.full, ch - 2, ch, x.budget_ns);
             break;
         }
         const uint8_t* blob = blobs + int64_t(ch) * kBlob;
@@ -711,7 +718,18 @@ __device__ __forceinline__ void run_loaders(Sm& sm, const ChunkArgs& x, int lt, 
         scale_tile<DK, FIRST>(st.q, mq, f->qmul, lt);
         tc::mbar_arrive(&sm.full[s]);
     }
-    // the last copies land before the CTA may end: the scanning warps wait for every stage
+    // else the scanning warps wait for every stage, also those that give up
+}
+
+// What a scanning warp leaves that gave up waiting for chunk ch: NaN from its first token on for its channels.  Called, not
+// inlined, which costs the prefill form 2 %.
+__device__ __noinline__ void give_up(uint64_t* full, int ch, uint64_t budget_ns, bf16* o, int64_t channel, int64_t token, int cols,
+                                     int len) {
+    const int t0 = ch * C;
+    landed(full, ch, min(ch + 2, (len + C - 1) / C), budget_ns);
+    const bf16 nan = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+    for (int c = 0; c < cols; ++c)
+        for (int64_t t = t0 + int(threadIdx.x & 31); t < len; t += 32) o[c * channel + t * token] = nan;
 }
 
 // One element of a tile of 16-bit numbers [token][channel], or (FIRST) [channel][token].
@@ -878,15 +896,11 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         }
     bf16* ob = static_cast<bf16*>(a.o) + b * a.os.sb + (int64_t(h) * a.dv + dw) * a.os.sc;
     bf16* so = sm.o[warp];
-    for (int ch = 0; ch < chunks; ++ch) {
+    int ch = 0;
+    for (; ch < chunks; ++ch) {
         const int s = ch & 1;
         typename Sm::Stage& st = sm.st[s];
-        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) {
-            if (lane == 0) report_status(x.status, kStatusTimeout);
-#pragma unroll
-            for (int j = 0; j < DK / 8; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
-            break;
-        }
+        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) break;
         const int64_t t0 = int64_t(ch) * C;
         const int n = min(C, len - ch * C);
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
@@ -1131,7 +1145,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             }
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+        if (lane == 0 && ch != x.hold) tc::mbar_arrive(&sm.empty[s]);
         const int cols = min(16, a.dv - dw);
         bf16* oc = ob + t0 * a.os.st;
         if (x.vec_o && n == C && cols == 16) {
@@ -1176,6 +1190,12 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
             }
         }
         __syncwarp();
+    }
+    if (ch < chunks) {                             // gave up waiting
+        if (lane == 0) report_status(x.status, kStatusTimeout);
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
+        give_up(sm.full, ch, x.budget_ns, ob, a.os.sc, a.os.st, min(16, a.dv - dw), len);
     }
     if (a.state_out) {
 #pragma unroll
@@ -1305,15 +1325,11 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
         }
     bf16* ob = static_cast<bf16*>(a.o) + b * a.os.sb + (int64_t(h) * a.dv + dw) * a.os.sc;
     bf16* so = sm.o[warp];
-    for (int ch = 0; ch < chunks; ++ch) {
+    int ch = 0;
+    for (; ch < chunks; ++ch) {
         const int s = ch & 1;
         typename Sm::Stage& st = sm.st[s];
-        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) {
-            if (lane == 0) report_status(x.status, kStatusTimeout);
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
-            break;
-        }
+        if (!tc::mbar_wait(&sm.full[s], uint32_t(ch >> 1) & 1u, x.budget_ns)) break;
         const int64_t t0 = int64_t(ch) * C;
         const int n = min(C, len - ch * C);
         const uint32_t tk = tc::smem_u32(st.k), tq = tc::smem_u32(st.q), tb = tc::smem_u32(st.blob);
@@ -1525,7 +1541,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             }
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.empty[s]);
+        if (lane == 0 && ch != x.hold) tc::mbar_arrive(&sm.empty[s]);
         const int cols = min(8, a.dv - dw);
         bf16* oc = ob + t0 * a.os.st;
         if (x.vec_o && n == C && cols == 8) {
@@ -1547,6 +1563,12 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
             }
         }
         __syncwarp();
+    }
+    if (ch < chunks) {                             // gave up waiting
+        if (lane == 0) report_status(x.status, kStatusTimeout);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = __int_as_float(0x7fffffff);
+        give_up(sm.full, ch, x.budget_ns, ob, a.os.sc, a.os.st, min(8, a.dv - dw), len);
     }
     if (a.state_out) {
 #pragma unroll
@@ -1633,12 +1655,14 @@ cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
 
 size_t delta_chunk_workspace(int64_t B, int64_t L, int Hv) { return size_t(B) * size_t(Hv) * size_t((L + C - 1) / C) * kBlob; }
 
-cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, cudaStream_t s) {
+cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* status, uint64_t budget_ns, int64_t hold,
+                               cudaStream_t s) {
     ChunkArgs x{};
     x.a = a;
     x.blobs = static_cast<uint8_t*>(workspace);
     x.chunks = int((a.L + C - 1) / C);
-    x.budget_ns = kDefaultWaitBudgetNs;
+    x.budget_ns = budget_ns;
+    x.hold = hold >= 0 && hold < x.chunks ? int(hold) : -1;
     x.status = status;
     cudaError_t e = device_sms(&x.dev, &x.sms);
     if (e != cudaSuccess) return e;

@@ -444,7 +444,8 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  * when that is 0); its contents are undefined after the call, and two calls
  * that may run at the same time need one each.  Asynchronous on `stream`,
  * may be captured into a graph.  A bounded device wait that runs out is
- * reported by hyena_kernel_status; the state of that head is NaN then.
+ * reported by hyena_kernel_status; the value channels that waited have NaN in
+ * o from the chunk they waited for on, and in state_out.
  */
 #define HYENA_DELTA_L2NORM 0x1u
 
@@ -635,6 +636,17 @@ hyena_status_t hyena_debug_conv_2d_tc(const void* u, void* y, const void* spectr
 hyena_status_t hyena_debug_conv_2dc_tc(const void* u, void* y, const void* spectrum, size_t spectrum_bytes, int64_t B,
                                        int64_t C, int order, void* workspace, size_t workspace_bytes,
                                        uint64_t wait_budget_ns, int issue_mma, void* stream);
+
+/*
+ * The same test hook for the scans of hyena_delta_rule in chunks (bf16, more
+ * than 16 tokens): their waits give up after wait_budget_ns, and the stage of
+ * chunk `hold_chunk` (64 tokens each; -1: none) is never freed, so the wait for
+ * chunk hold_chunk + 2 runs out where there is one.  The timeout is recorded, o
+ * is NaN from that chunk on, state_out is NaN.  Arguments that do not run in
+ * chunks return HYENA_ERR_UNSUPPORTED_SHAPE.
+ */
+hyena_status_t hyena_debug_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
+                                      uint64_t wait_budget_ns, int64_t hold_chunk, void* stream);
 
 #ifdef __cplusplus
 }
