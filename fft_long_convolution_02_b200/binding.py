@@ -29,7 +29,7 @@ EXPORTS = ["hyena_version", "hyena_status_string", "hyena_last_error_detail", "h
            "hyena_debug_conv_tc", "hyena_debug_conv_cluster", "hyena_debug_conv_2d_tc", "hyena_debug_conv_2dc_tc", "hyena_gated_fftconv_ex", "hyena_kernel_status", "hyena_in_proj",
            "hyena_out_proj", "hyena_implicit_filter_workspace_bytes", "hyena_filter_spectrum_implicit",
            "hyena_delta_rule_workspace_bytes", "hyena_delta_rule", "hyena_delta_rule_step", "hyena_quantize_fp8",
-           "hyena_quantize_fp8_weight", "hyena_proj_fp8", "hyena_debug_delta_rule"]
+           "hyena_quantize_fp8_weight", "hyena_proj_fp8", "hyena_debug_delta_rule", "hyena_debug_proj_fp8"]
 
 _lock = threading.Lock()
 _lib = None
@@ -125,6 +125,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.hyena_quantize_fp8_weight.argtypes = [vp, vp, fp, i64, i64, ctypes.c_int, vp]
         lib.hyena_proj_fp8.restype = ctypes.c_int
         lib.hyena_proj_fp8.argtypes = [vp, fp, vp, fp, fp, vp, i64, i64, i64, i64, ctypes.c_int, vp]
+        lib.hyena_debug_proj_fp8.restype = ctypes.c_int
+        lib.hyena_debug_proj_fp8.argtypes = [vp, fp, vp, fp, fp, vp, i64, i64, i64, i64, ctypes.c_int, ctypes.c_uint64,
+                                             ctypes.c_int, vp]
         _lib = lib
     return _lib
 
@@ -438,11 +441,8 @@ def hyena_quantize_fp8_weight(W, Wq, Ws, stream=None) -> None:
                                             _raw_stream(stream, dev)))
 
 
-def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stream=None) -> None:
-    """xq [B, L, K], Wq [N, K] float8_e4m3fn with their scales, bias [N] f32 or
-    None -> out bf16 [B, L, N], or [B, N, L] with channels_first."""
-    torch = _lazy_torch()
-    dev = _on_device(xq, xs, Wq, Ws, bias, out)
+def _proj_fp8_sizes(xq, xs, Wq, Ws, bias, out, channels_first):
+    torch = _torch
     B, L, K = xq.shape
     N = Wq.shape[0]
     _plain("xq", xq, (B, L, K), torch.float8_e4m3fn)
@@ -451,6 +451,15 @@ def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stre
     _plain("Ws", Ws, (-(-N // 128), -(-K // 128)), torch.float32)
     _plain("bias", bias, (N,), torch.float32)
     _plain("out", out, (B, N, L) if channels_first else (B, L, N), torch.bfloat16)
+    return B, L, K, N
+
+
+def hyena_proj_fp8(xq, xs, Wq, Ws, bias, out, channels_first: bool = False, stream=None) -> None:
+    """xq [B, L, K], Wq [N, K] float8_e4m3fn with their scales, bias [N] f32 or
+    None -> out bf16 [B, L, N], or [B, N, L] with channels_first."""
+    _lazy_torch()
+    dev = _on_device(xq, xs, Wq, Ws, bias, out)
+    B, L, K, N = _proj_fp8_sizes(xq, xs, Wq, Ws, bias, out, channels_first)
     _check(load().hyena_proj_fp8(xq.data_ptr(), xs.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), _ptr(bias),
                                  out.data_ptr(), B, L, K, N, 1 if channels_first else 0, _raw_stream(stream, dev)))
 
@@ -555,3 +564,14 @@ def hyena_debug_delta_rule(q, k, v, g, beta, o, Hk: int, Hv: int, state_in, stat
     _, _, packed = _delta_args(q, k, v, g, beta, o, B, L, Hk, Hv, None, l2norm, (state_in, state_out, None), True)
     _check(load().hyena_debug_delta_rule(packed, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                          int(wait_budget_ns), hold_chunk, _raw_stream(stream, dev)))
+
+
+def hyena_debug_proj_fp8(xq, xs, Wq, Ws, bias, out, wait_budget_ns: int, hold: int = 0, channels_first: bool = False,
+                         stream=None) -> None:
+    """The same test hook for hyena_proj_fp8 (more than 16 rows): hold 1 issues no products, 2 keeps a warp's staged part back."""
+    _lazy_torch()
+    dev = _on_device(xq, xs, Wq, Ws, bias, out)
+    B, L, K, N = _proj_fp8_sizes(xq, xs, Wq, Ws, bias, out, channels_first)
+    _check(load().hyena_debug_proj_fp8(xq.data_ptr(), xs.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), _ptr(bias), out.data_ptr(),
+                                       B, L, K, N, 1 if channels_first else 0, int(wait_budget_ns), hold,
+                                       _raw_stream(stream, dev)))

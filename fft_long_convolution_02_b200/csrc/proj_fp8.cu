@@ -76,7 +76,11 @@ struct Params {
     int channels_first, store;
     uint64_t budget_ns;
     uint32_t* status;
+    int hold;                                     // test hook
 };
+
+// What the test hook withholds: nothing, the products, or a warp's word that its part of a tile is staged.
+enum Hold { HOLD_NONE = 0, HOLD_PRODUCTS = 1, HOLD_STAGED = 2 };
 
 // BN columns a tile; G CTAs share one (G = 2: 256 rows).
 template <int BN, int G>
@@ -217,6 +221,25 @@ __device__ __forceinline__ float2 unpair(uint64_t x) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
     return f;
 }
+// A reading warp that gave up at `tile`: NaN for its rows and columns of that tile and of the CTA's later ones; `whole_half`
+// for the rows of all four warps in the first.
+template <int BN, int G>
+__device__ __noinline__ void give_up(const Params p, int tile, int tiles, int step, int rank, int q, int half, bool whole_half) {
+    constexpr int CW = Cfg<BN, G>::CW;
+    const bf16 nan = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+    for (; tile < tiles; tile += step, whole_half = false) {
+        int tm, tn;
+        place(p, tile, tm, tn);
+        const int64_t n0 = int64_t(tn) * BN + half * CW;
+        for (int w = whole_half ? 0 : q; w <= (whole_half ? 3 : q); ++w) {
+            const int64_t m = (int64_t(tm) * G + rank) * BM + 32 * w + int(threadIdx.x & 31);
+            if (m >= p.M) continue;
+            const int64_t b = uint32_t(m) / uint32_t(p.L), l = m - b * p.L;
+            for (int i = 0; i < CW && n0 + i < p.N; ++i) p.out[p.channels_first ? (b * p.N + n0 + i) * p.L + l : m * p.N + n0 + i] = nan;
+        }
+    }
+}
+
 template <int BN, int G>
 __global__ void __launch_bounds__(kThreads, 1)
 k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -329,7 +352,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     const uint32_t d = tmem + uint32_t(acc) * BN;
                     // the tail of the last block lies behind K: zeros, and no products for whole steps of them
                     const int steps = kb + 1 < p.kblocks ? 4 : tail;
-                    if (elect_one()) {
+                    if (p.hold != HOLD_PRODUCTS && elect_one()) {
                         mma_e4m3<G>(d, da, db, idesc, 0u);
                         if (steps > 1) mma_e4m3<G>(d, da + 2, db + 2, idesc, 1u);
                         if (steps > 2) mma_e4m3<G>(d, da + 4, db + 4, idesc, 1u);
@@ -428,8 +451,9 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
         float* bias = s_bias + (warp - 4) * CW;
         int buf = 0, s = 0;
         uint32_t phase = 0, out_phase = 0;
-        bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
+        bool ok = true, whole_half = false;
+        int tile = first;
+        for (; tile < tiles; tile += step) {
             int tm, tn;
             place(p, tile, tm, tn);
             const int64_t m0 = (int64_t(tm) * G + rank) * BM + 32 * q, m = m0 + lane;
@@ -477,11 +501,7 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                     phase ^= 1u;
                 }
             }
-            if (!ok) {                            // a wait ran out: NaN for this row's outputs
-                for (int i = 0; live && i < CW && n0 + i < p.N; ++i)
-                    p.out[p.channels_first ? (b * p.N + n0 + i) * p.L + l : m * p.N + n0 + i] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
-                break;
-            }
+            if (!ok) break;
             // the warp's own copy: no barrier that a warp which gave up would leave others at
             __syncwarp();
 #pragma unroll
@@ -574,9 +594,10 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (p.channels_first) {
-                    if (lane == 0) tc::mbar_arrive(&out_full[half]);
+                    if (lane == 0 && (p.hold != HOLD_STAGED || q != 1)) tc::mbar_arrive(&out_full[half]);
                     if (q == 0 && !tc::mbar_wait(&out_full[half], out_phase, p.budget_ns)) {
                         ok = false;
+                        whole_half = true;        // the other warps may be past this tile: theirs do not leave either
                         break;
                     }
                     out_phase ^= 1u;
@@ -601,7 +622,10 @@ k_proj_fp8(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CU
                 }
             }
         }
-        if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
+        if (!ok) {
+            if (lane == 0) report_status(p.status, kStatusTimeout);
+            give_up<BN, G>(p, tile, tiles, step, rank, q, half, whole_half);
+        }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
     __syncwarp();
@@ -783,9 +807,10 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 using namespace hyena;
 
-extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws,
-                                         const float* bias, void* out, int64_t B, int64_t L, int64_t K, int64_t N,
-                                         int channels_first, void* stream) {
+namespace {
+
+hyena_status_t run(const void* xq, const float* xs, const void* Wq, const float* Ws, const float* bias, void* out, int64_t B,
+                   int64_t L, int64_t K, int64_t N, int channels_first, uint64_t budget_ns, int hold, void* stream) {
     if (!xq || !xs || !Wq || !Ws || !out) return fail(HYENA_ERR_INVALID_ARG, "xq, xs, Wq, Ws and out must not be NULL");
     if (B < 1 || L < 1 || K < 1 || N < 1) return fail(HYENA_ERR_INVALID_ARG, "B, L, K and N must be >= 1");
     if (K % 16 != 0 || K > (int64_t(1) << 20) || N > (int64_t(1) << 20) || B > 65535 || L > (int64_t(1) << 31) - 1 ||
@@ -805,7 +830,7 @@ extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const 
         return fail(HYENA_ERR_INVALID_ARG, "out overlaps an input");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Params p{M, L, N, K, int(kblocks), 0, 0, xs, Ws, bias, static_cast<bf16*>(out), channels_first != 0, STORE_PLAIN,
-             kDefaultWaitBudgetNs, nullptr};
+             budget_ns, nullptr, hold};
     if (M <= kFewTokens) {
         const unsigned grid = unsigned((N + 15) / 16);
         const uint8_t *x = static_cast<const uint8_t*>(xq), *w = static_cast<const uint8_t*>(Wq);
@@ -824,4 +849,22 @@ extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const 
     if (tm * ((N + 255) / 256) >= sms) return launch<256, 2>(xq, Wq, p, dev, sms, s);
     if (tm * ((N + 127) / 128) >= sms) return launch<128, 1>(xq, Wq, p, dev, sms, s);
     return launch<64, 1>(xq, Wq, p, dev, sms, s);
+}
+
+}  // namespace
+
+extern "C" hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws,
+                                         const float* bias, void* out, int64_t B, int64_t L, int64_t K, int64_t N,
+                                         int channels_first, void* stream) {
+    return run(xq, xs, Wq, Ws, bias, out, B, L, K, N, channels_first, kDefaultWaitBudgetNs, HOLD_NONE, stream);
+}
+
+extern "C" hyena_status_t hyena_debug_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws,
+                                               const float* bias, void* out, int64_t B, int64_t L, int64_t K, int64_t N,
+                                               int channels_first, uint64_t wait_budget_ns, int hold, void* stream) {
+    if (wait_budget_ns == 0) return fail(HYENA_ERR_INVALID_ARG, "wait_budget_ns must be > 0");
+    if (hold < HOLD_NONE || hold > HOLD_STAGED) return fail(HYENA_ERR_INVALID_ARG, "hold must be 0, 1 or 2");
+    if (B >= 1 && B <= kFewTokens && L >= 1 && L <= kFewTokens && B * L <= kFewTokens)
+        return fail(HYENA_ERR_UNSUPPORTED_SHAPE, "a few rows have no waits");
+    return run(xq, xs, Wq, Ws, bias, out, B, L, K, N, channels_first, wait_budget_ns, hold, stream);
 }

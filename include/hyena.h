@@ -527,7 +527,9 @@ hyena_status_t hyena_quantize_fp8_weight(const void* W, void* Wq, float* Ws, int
  * K a multiple of 16, L and N any, B <= 65535, B * L <= 2^31 - 1, N and K <= 2^20, out of fewer than
  * 2^31 tiles of 128 x 64; xq, Wq, out
  * 16-byte aligned, xs, Ws, bias 4-byte; out may not overlap an input.  A
- * bounded device wait that runs out is reported by hyena_kernel_status.
+ * bounded device wait that runs out is reported by hyena_kernel_status; the
+ * tiles of out that waited are NaN.  The product of two scales is an fp32
+ * number too: below 2^-126 it loses bits, above fp32's range it is infinite.
  */
 hyena_status_t hyena_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws, const float* bias,
                               void* out, int64_t B, int64_t L, int64_t K, int64_t N, int channels_first,
@@ -647,6 +649,17 @@ hyena_status_t hyena_debug_conv_2dc_tc(const void* u, void* y, const void* spect
  */
 hyena_status_t hyena_debug_delta_rule(const hyena_delta_rule_t* p, void* workspace, size_t workspace_bytes,
                                       uint64_t wait_budget_ns, int64_t hold_chunk, void* stream);
+
+/*
+ * The same test hook for hyena_proj_fp8 with more than 16 rows: its waits give
+ * up after wait_budget_ns.  hold = 0 withholds nothing, 1 the tensor-core
+ * products, 2 (channels_first with L a multiple of 128; no effect elsewhere) a warp's word that
+ * its part of a tile is staged for the store.  The timeout is recorded and out
+ * is NaN.  Fewer rows return HYENA_ERR_UNSUPPORTED_SHAPE.
+ */
+hyena_status_t hyena_debug_proj_fp8(const void* xq, const float* xs, const void* Wq, const float* Ws, const float* bias,
+                                    void* out, int64_t B, int64_t L, int64_t K, int64_t N, int channels_first,
+                                    uint64_t wait_budget_ns, int hold, void* stream);
 
 #ifdef __cplusplus
 }
