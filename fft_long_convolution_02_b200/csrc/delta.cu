@@ -362,8 +362,12 @@ bool meets_operand(const Range& r, const hyena_delta_rule_t* p) {
            (p->lengths && r.meets(flat(p->lengths, 4 * p->B)));
 }
 
-// bf16 storage runs in chunks from a few tokens on; below, one launch of the token-by-token kernel is sooner done (four
-// heads of 64: 9.4 us at 16 tokens, where the chunked form takes 13; 22.3 against 12.1 us at 64).
+// bf16 storage runs in chunks from a few tokens on.  Where the two forms cross depends on the heads in flight (us of a call,
+// token by token against chunks, token-major rows): 4 heads of 64 10.5 against 14.4 at 20 tokens, 14.4 against 14.4 at 32,
+// 22.9 against 13.6 at 64; 256 heads of 128 40 against 39 at 16, 66 against 39 at 32; 1024 heads of 128 148 against 130 at 16,
+// 245 against 133 at 32.  (Rows along time that do not start on 16 bytes cost the chunks 5 us more: 17 tokens of 4 heads 12.4
+// against 19.3.)  The border lies at the lowest of these, by the length alone, so that a sequence's results do not depend on
+// how many others are in the call: few heads lose up to 4 us (7 unaligned) from 17 to 31 tokens by it.
 constexpr int64_t kSeqMost = 16;
 bool chunked(int64_t L, int dtype) { return dtype == HYENA_BF16 && L > kSeqMost; }
 

@@ -207,11 +207,12 @@ __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
 // diagonal by substitution (a thread a column, the columns in registers), then
 // twice the block under two inverses as -T22 (A21 T11).  Its chain of short
 // steps bounds it, so what counts is how many CTAs an SM holds: A and T lie
-// where K and Q were, five to an SM.  22 ns a chunk (dk = 128, 16384 chunks
-// 359 us; 611 us with three CTAs an SM and 32 x 32 substitutions), 53 % of the
-// issue slots; six CTAs with half of the products at a time were slower (82
-// against 73 us for 3072 chunks).  GROUP: up to four value heads of a key head
-// one after the other from the same products.
+// where K and Q were, five to an SM.  25 ns a chunk (dk = 128, 3072 chunks
+// 78 us), 45 % of the issue slots.  Three CTAs an SM with 32 x 32 substitutions
+// took 1.7 times as long, six CTAs with half of the products at a time 1.1
+// times.  GROUP: up to four value heads of a key head one after the other from
+// the same products (8192 chunks of two heads, dk = 128: 337 us); ptxas then
+// spills 72 bytes a thread (dk = 64: 224), 0 without.
 constexpr int kPrepThreads = 128;
 constexpr int kGroup = kPrepThreads / 32;          // most value heads of a CTA: a warp sums one's decays
 constexpr int kARow = 68;
@@ -533,10 +534,11 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
 // to registers here, where each of tcgen05's would wait for a commit, a read of
 // tensor memory, the split into two parts and a store of it.
 // A chunk of 128 channels takes 11900 cycles for 6400 of products (eight warps,
-// 43 % of the tensor pipe, 38 % of the issue slots), of 64 channels 7100 for
+// 43 % of the tensor pipe, 39 % of the issue slots), of 64 channels 7500 for
 // 3200: the splits and scalings between the products of an in-order warp bound
-// it, and the registers of the state the number of warps.  256 heads of 64
-// chunks 906 us.
+// it, and the registers of the state the number of warps (with eight, dk = 128,
+// 72 to 88 bytes a thread are spilled, with four 44 to 64).  256 heads of 64
+// chunks 908 us.
 constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
 constexpr int kORow = 16;                          // elements of a token's row of a warp's outputs
@@ -1216,9 +1218,10 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
 //   X = K S,  R = V - diag(cx) X,  U = T R,  S = gamma S + K^T (diag(cu) U),  O = diag(co) Q S + P U,
 // and a result becomes the next one's right operand by transposing its 8 x 8
 // blocks in registers.  Every warp reads all of K, Q, T and P as left operands,
-// so shared memory would bound more than four warps an SM.  A chunk takes 5100
+// so shared memory would bound more than four warps an SM.  A chunk takes 5500
 // cycles, the warp's and its scheduler's loading warp's issue slots two thirds
-// of them: 24 heads of 128 chunks 350 us (500 us with 16 channels a warp).
+// of them: 24 heads of 128 chunks 376 us (500 us with 16 channels a warp).  One
+// CTA an SM: 255 registers (dk = 64: 225) and half of the shared memory.
 constexpr int kNarrowWarps = 4, kNarrowCols = 8 * kNarrowWarps;
 constexpr int kNarrowVRow = kNarrowCols + 8;       // elements of a token's row of V: eight rows on 32 banks
 
@@ -1638,15 +1641,19 @@ template <int DK, bool FIRST>
 cudaError_t launch_both(const ChunkArgs& x, cudaStream_t s) {
     cudaError_t e = x.group > 1 ? launch_prep<DK, FIRST, true>(x, s) : launch_prep<DK, FIRST, false>(x, s);
     if (e != cudaSuccess) return e;
-    // A chunk takes a CTA of 32, 64 or 128 channels about 5100, 7100 or 11900 cycles (dk = 128): the form whose waves of
-    // CTAs take least.  Measured at L = 1024, dk = dv = 128, us by width: 32 heads 65, 82, 115; 72 heads 128, 107, 133;
-    // 144 heads 246, -, 160.
+    // A chunk takes a CTA of 32, 64 or 128 channels about 5500, 7500 or 11900 cycles (dk = 128): the form whose waves of
+    // CTAs take least.  dk = 64 takes less, but in nearly the same proportion.  Measured at L = 1024, token by token rows, us
+    // of a call by width:
+    //   heads            32            72            144            256            512
+    //   dk = dv = 128    65  92 135   128 117 150   244 217 179    418 394 332    822 725 646
+    //   64, dv = 128     51  68 100    97  81 112   186 156 138    315 276 254    619 515 497
+    //   dk = dv = 64     50  66  99    62  80 111   121 104 137    219 183 252    395 352 494
     const int64_t heads = x.a.B * x.a.Hv;
     auto cycles = [&](int width, int64_t each) {
         const int64_t ctas = heads * ((x.a.dv + width - 1) / width);
         return (ctas + x.sms - 1) / x.sms * each;
     };
-    const int64_t narrow = cycles(32, 5100), half = cycles(64, 7100), full = cycles(128, 11900);
+    const int64_t narrow = cycles(32, 5500), half = cycles(64, 7500), full = cycles(128, 11900);
     if (narrow <= half && narrow <= full) return launch_narrow<DK, FIRST>(x, s);
     return half <= full ? launch_scan<DK, 4, FIRST>(x, s) : launch_scan<DK, 8, FIRST>(x, s);
 }
@@ -1668,8 +1675,9 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* workspace, uint32_t* st
     if (e != cudaSuccess) return e;
     // the tiles lie as the keys do: along time where that is their contiguous axis
     const bool first = a.ks.st == 1 || a.ks.sc != 1;
-    // Value heads of one key head share its products, once that leaves every SM its five CTAs (8192 chunks of two heads each
-    // 316 us against 359 us one by one); few chunks are sooner done one by one.
+    // Value heads of one key head share its products, once that leaves every SM its five CTAs.  Calls with and without, us:
+    // 16 x 4096, 8 key heads of 2: 1203, 1230 (dk = 64: 676, 682); 16 x 2048, 4 of 4: 603, 628 (337, 349); 8 x 2048, 4 of 2,
+    // just above the border: 207, 204 (114, 109).  Fewer chunks are sooner done one by one (2 x 1024, 4 of 2: 66, 60).
     const int r = a.Hv / a.Hk;
     x.group = 1;
     for (int n = 2; n <= kGroup; ++n)

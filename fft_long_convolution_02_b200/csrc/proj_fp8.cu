@@ -29,7 +29,8 @@
 // tile's first blocks.  What bounds it: two buffers of sums are all that tensor
 // memory holds, and a buffer's round trip (512 cycles of products, arrivals
 // across the pair, reading, arrivals again) is longer than two blocks' products.
-// 32768 x 2048 x 4096: 297 us, 1.85 PFLOP/s; 32768 x 768 x 2304: 85 us, 1.36.
+// A call among others, inputs from DRAM: 32768 x 2048 x 4096 345 us, 1.59 PFLOP/s; 32768 x 768 x 2304 100 us, 1.15 (on its
+// own, inputs in L2, clocks at their highest: 297 us, 1.85; 85 us, 1.36).
 //
 // k_proj_fp8_few (up to kFewTokens rows): the weights' bytes bound it.  A CTA
 // takes 16 outputs; its 8 warps take the blocks of K in turn, W as the 16-row

@@ -5,7 +5,11 @@
 //
 // Both are one pass over x, bound by its bytes in and the e4m3 bytes out: a
 // block's values stay in registers between the maximum and the rounding.
-// 32768 x 768 bf16: 19.7 us, 3.9 TB/s.
+// 32768 x 768 bf16: 19.7 us, 3.9 TB/s (channels contiguous), 26.7 us, 2.9 TB/s
+// (positions contiguous).  17 instructions an element bound it (unpacking, the
+// maximum, the corrected quotient, the conversion): 71 % of the issue slots, 53 %
+// where the tile goes through shared memory.  Weights: 2304 x 768 6.2 us,
+// 16384 x 2048 29 us (floors 0.8 and 15.6).
 // The maximum is taken over the bits of |x|, which order like the values and
 // put NaN above infinity, so a NaN reaches the scale.
 #include <cuda_bf16.h>
