@@ -207,7 +207,7 @@ __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
 // diagonal by substitution (a thread a column, the columns in registers), then
 // twice the block under two inverses as -T22 (A21 T11).  Its chain of short
 // steps bounds it, so what counts is how many CTAs an SM holds: A and T lie
-// where K and Q were, five to an SM.  25 ns a chunk (dk = 128, 3072 chunks
+// where K and Q were, five to an SM.  25 ns a chunk (dk = 128; 4 x 8192, 6 heads
 // 78 us), 45 % of the issue slots.  Three CTAs an SM with 32 x 32 substitutions
 // took 1.7 times as long, six CTAs with half of the products at a time 1.1
 // times.  GROUP: up to four value heads of a key head one after the other from
@@ -559,9 +559,12 @@ constexpr int kORow = 16;                          // elements of a token's row 
 //   outputs  the writes, key and decay with them, below 2^-28 of the largest write
 //            and key at the end of the chunk; the chunk's first write, or two
 //            neighbouring writes, below 2^-28 of the largest.
-// A single write far below the others is left alone: their terms make the output,
-// and chance brings one in 10^4 chunks.  Looking for all this costs 1 % (16 x 4096
-// x 16 heads 1195 -> 1204 us) to 2 % (4 x 8192 x 6 heads 433 -> 442 us).
+// A single write far below the others is left alone: mostly their terms make the
+// output, and chance brings one in 10^4 chunks.  (Where a strong decay has emptied
+// those terms too, that one output, below 2^-28 of its neighbours', loses bits.)
+// Looking for all this costs 1 % (16 x 4096 x 16 heads 1195 -> 1204 us) to 2 %
+// (4 x 8192 x 6 heads 433 -> 442 us), at dk = 64 5 % (144 heads of 16 chunks 94 ->
+// 99 us).
 __device__ __forceinline__ bool below(float write, float largest) { return write != 0.0f && write < largest * 0x1p-28f; }
 
 template <int DK, int VR, int VC>

@@ -428,7 +428,10 @@ hyena_status_t hyena_out_proj(const void* y, const void* W, const float* bias, v
  *             tokens' outputs or the state would lose more than that, the
  *             chunk runs token by token instead, some 15 times as long.  A
  *             channel that gates shrink by 2^18 to 2^24 within a chunk keeps 2^-20
- *             to 2^-16 of itself.  An infinity or NaN among a row's own
+ *             to 2^-16 of itself, and a single token whose output lies below
+ *             2^-28 of the channel's largest write nearby (one that is masked
+ *             under a strong decay, say) may have that output in fewer bits, or
+ *             0.  An infinity or NaN among a row's own
  *             tokens can reach the outputs of up to 63 tokens before it, and
  *             keys or queries below 1e-18 in norm lose bits.  In all forms the
  *             square of a key's or query's norm is an fp32 number: norms above

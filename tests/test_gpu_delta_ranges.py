@@ -184,3 +184,31 @@ def test_magnitudes_far_apart_without_norms_or_gates(layout):
     for ch in ([7], [d for d in range(64) if d != 7]):
         assert _rel(n[..., ch], ref[1][..., ch]) <= STATE(64, 100)
     assert torch.isfinite(s1).all()
+
+
+@pytest.mark.parametrize("layout", ["first", "last"])
+@pytest.mark.parametrize("B,L,Hk,Hv,dk,dv", [(1, 150, 1, 2, 64, 64), (40, 66, 2, 4, 64, 64), (19, 100, 2, 4, 128, 120)])
+def test_far_apart_without_gate_tensors_and_with_a_scale(B, L, Hk, Hv, dk, dv, layout):
+    """No gates (as zeros and ones), a scale of one's own, the state in place, no final state wanted: the same outputs."""
+    import torch
+    c = Case(B, L, Hk, Hv, dk, dv, layout=layout, gates=False)
+    c.v.unflatten(1, (Hv, dv))[:, :, 3, 40] = 1e12
+    o, s1 = c.run(scale=0.25)
+    half, _ = c.run(scale=0.125)
+    assert torch.equal(o, half * 2)
+    s = c.s0.clone()
+    o2, _ = c.run(scale=0.25, state_in=s, state_out=s)
+    assert torch.equal(o2, o) and torch.equal(s, s1)
+    o3, _ = c.run(scale=0.25, state_out=None)
+    assert torch.equal(o3, o)
+    c.g, c.beta = torch.zeros(B, Hv, L, device="cuda"), torch.ones(B, Hv, L, device="cuda")
+    o4, s4 = c.run(scale=0.25)
+    assert torch.equal(o4, o) and torch.equal(s4, s1)
+    ro, rs = c.oracle(scale=0.25)
+    rest = [d for d in range(dv) if d != 3]
+    for ch in ([3], rest):
+        assert _rel(_np(s1)[..., ch], rs[..., ch]) <= STATE(dk, L)
+    early = _np(o).reshape(B, Hv, dv, L)[:, :, 3, :40]             # before the large value, whose channel they share
+    ref = ro.reshape(B, Hv, dv, L)[:, :, 3, :40]
+    mag, read = (x[:, :, 3, :40] * 0.25 * dk ** 0.5 for x in terms(c))
+    assert (np.abs(early - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + STATE(dk, L) * read).all()
