@@ -42,17 +42,16 @@ using bf16 = __nv_bfloat16;
 
 constexpr int C = 64;                              // tokens of a chunk
 
-// Bounds that tell a chunk whose magnitudes lie too far apart (see the scans).  u, r: a channel's largest write and
-// residual; n: its largest entry of U diag(cu); s: of the state before the chunk.
-struct alignas(16) Reach {
-    float w, k;                                    // T's largest times what its row's write leaves in the state; the largest key
-    int first;                                     // the first token that writes (C: none)
-    __device__ __forceinline__ bool end(float u, float r, float n, float s, float gamma) const {
-        return fmaxf(n * 0x1p14f, gamma * s) < fmaxf(r * w, u * k);
+// Bounds that tell a chunk whose magnitudes lie too far apart (see the scans).  m: the larger of a channel's largest write
+// and of its largest residual times T's largest; r: that residual; n: the largest entry of U diag(cu); s: of the state
+// before the chunk.
+struct Reach {
+    float t, w, k;                                 // T's largest; times what its row's write leaves in the state; the largest key
+    __device__ __forceinline__ bool end(float m, float r, float n, float s, float gamma) const {
+        return fmaxf(n * 0x1p14f, gamma * s) < fmaxf(r * w, m * k);
     }
-    __device__ __forceinline__ bool start(float u_first, float u, float s, float gamma) const {
-        return u_first < u * 0x1p-28f && fminf(gamma, 1.0f) * s < u * k;
-    }
+    // whether outputs rest on the chunk's writes: the state before it is as small as they may be
+    __device__ __forceinline__ bool bare(float m, float s, float gamma) const { return fminf(gamma, 1.0f) * s < m * k; }
 };
 
 // What k_delta_prep leaves for a chunk of a value head: T's two parts and P as
@@ -64,9 +63,9 @@ struct Factors {
     float co[C];                                   // (Q S) row of the scaled Q to the output
     float cp[C], ct[C];                            // rows of the stored P and T to P and T
     float gamma;                                   // e^{G_63}
-    float pad0[3];
     Reach reach;
-    float pad[56];
+    uint32_t strong[2];                            // tokens whose write strength is not 0, a bit each
+    float pad[58];
 };
 constexpr uint32_t kTile = C * C * 2;              // bytes of a 64 x 64 fp16 image
 constexpr uint32_t kBlob = 3 * kTile + uint32_t(sizeof(Factors));
@@ -212,7 +211,7 @@ __device__ __forceinline__ int64_t length_of(const DeltaArgs& a, int64_t b) {
 // took 1.7 times as long, six CTAs with half of the products at a time 1.1
 // times.  GROUP: up to four value heads of a key head one after the other from
 // the same products (8192 chunks of two heads, dk = 128: 337 us); ptxas then
-// spills 72 bytes a thread (dk = 64: 224), 0 without.
+// spills 72 bytes a thread (dk = 64: 224), 4 at most without.
 constexpr int kPrepThreads = 128;
 constexpr int kGroup = kPrepThreads / 32;          // most value heads of a CTA: a warp sums one's decays
 constexpr int kARow = 68;
@@ -233,7 +232,6 @@ struct PrepSmem {
     alignas(16) float rk[C], rq[C], kn[C], qn[C];                  // norms' inverses (rq times the scale), norms
     float left[C];                                 // what a token's write leaves at the chunk's end, times its key
     float kmost[2];                                // largest of the scaled keys, by halves of the chunk
-    int first[2];                                  // first token that writes, by halves (C: none)
     float strict[kGroup];                          // 2^-24, or 2^-18 where a gate grows the state
 };
 
@@ -404,14 +402,14 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         f->co[t] = into * sm.rq[t] * pq.down;
         if (t == 0) {
             f->gamma = exp2f(gh[C - 1] + gl[C - 1]);
-            f->reach.w = 0.0f;
+            f->reach.t = f->reach.w = 0.0f;
         }
         sm.left[t] = out * sm.rk[t] * sm.kn[t];
         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(sm.rk[t] * sm.kn[t]));      // not negative
-        const unsigned writes = __ballot_sync(0xffffffffu, beta[t] != 0.0f && sm.kn[t] > 1e-18f);
+        const uint32_t strong = __ballot_sync(0xffffffffu, beta[t] != 0.0f);
         if (lane == 0) {
             sm.kmost[warp] = __uint_as_float(most);
-            sm.first[warp] = writes ? 32 * warp + __ffs(int(writes)) - 1 : C;
+            f->strong[warp] = strong;
         }
     }
     {
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             if (nt > 2 * warp + 1) break;          // what lies right of the diagonal's blocks is not read
             const int c = 8 * nt + 2 * t4;
             const float2 hc = *reinterpret_cast<const float2*>(&gh[c]), lc = *reinterpret_cast<const float2*>(&gl[c]);
-            const float2 rc = *reinterpret_cast<const float2*>(&sm.rk[c]);
+            const float2 rc = *reinterpret_cast<const float2*>(&sm.rk[c]), bc = *reinterpret_cast<const float2*>(&beta[c]);
             const float d[4] = {exp2f((h0 - hc.x) + (l0 - lc.x)) * rc.x, exp2f((h0 - hc.y) + (l0 - lc.y)) * rc.y,
                                 exp2f((h1 - hc.x) + (l1 - lc.x)) * rc.x, exp2f((h1 - hc.y) + (l1 - lc.y)) * rc.y};
             float av[4], pv[4];
@@ -433,7 +431,8 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
             for (int j = 0; j < 4; ++j) {
                 const int r = j < 2 ? r0 : r1, cc = c + (j & 1);
                 av[j] = cc < r ? (j < 2 ? a0 : a1) * d[j] * ka[nt][j] : 0.0f;
-                pv[j] = cc <= r ? d[j] * (j < 2 ? q0 : q1) * qa[nt][j] : 0.0f;
+                // what is never written is not read either, and does not set the row's scale
+                pv[j] = cc <= r && ((j & 1) ? bc.y : bc.x) != 0.0f ? d[j] * (j < 2 ? q0 : q1) * qa[nt][j] : 0.0f;
             }
             m0 = fmaxf(m0, fmaxf(fabsf(pv[0]), fabsf(pv[1])));
             m1 = fmaxf(m1, fmaxf(fabsf(pv[2]), fabsf(pv[3])));
@@ -500,12 +499,13 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
         const Pow2 p(m);
         if (c0 == 0) f->ct[r] = p.down;
         // not negative, so ordered as their bits; NaN above all, and then no comparison holds
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(m * sm.left[r])));
-        if (lane == 0) atomicMax(reinterpret_cast<uint32_t*>(&f->reach.w), __float_as_uint(__uint_as_float(w) * sm.strict[hh]));
-        if (tid == 0) {
-            f->reach.k = fmaxf(sm.kmost[0], sm.kmost[1]) * 0x1p-28f;
-            f->reach.first = min(sm.first[0], sm.first[1]);
+        if (lane == 0) {
+            atomicMax(reinterpret_cast<uint32_t*>(&f->reach.t), most);
+            atomicMax(reinterpret_cast<uint32_t*>(&f->reach.w), __float_as_uint(__uint_as_float(w) * sm.strict[hh]));
         }
+        if (tid == 0) f->reach.k = fmaxf(sm.kmost[0], sm.kmost[1]) * 0x1p-28f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (c0 + 8 * i > (r | 15)) break;
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) k_delta_prep(ChunkArgs x) {
 // 43 % of the tensor pipe, 39 % of the issue slots), of 64 channels 7500 for
 // 3200: the splits and scalings between the products of an in-order warp bound
 // it, and the registers of the state the number of warps (with eight, dk = 128,
-// 72 to 88 bytes a thread are spilled, with four 44 to 64).  256 heads of 64
+// 100 to 128 bytes a thread are spilled, with four 32 to 84).  256 heads of 64
 // chunks 908 us.
 constexpr int kLoaders = 128;
 constexpr int kVRow = 72;                          // elements of a V^T row: pairs of 8 rows on 32 banks
@@ -556,16 +556,19 @@ constexpr int kORow = 16;                          // elements of a token's row 
 //            residual times the largest of T (2^-18 where gates grow the state):
 //            above that the errors of U, 2^-39 of those, stay within 2^-16 of the
 //            state (measured: 2^-22 up to ratios of 2^18, 2^-20 at 2^20, 2^-16 at 2^24);
-//   outputs  the writes, key and decay with them, below 2^-28 of the largest write
-//            and key at the end of the chunk; the chunk's first write, or two
-//            neighbouring writes, below 2^-28 of the largest.
+//   outputs  what remains of the state and of the writes, key and decay with them,
+//            below 2^-28 of the largest write and key; or, where the state before
+//            the chunk is below that too, the first write or two neighbouring ones
+//            below 2^-28 of the largest.  (Largest write: or residual times T.)
+// Three looks: the smallest write of all, which zeros trip; without the tokens of
+// write strength 0; by channel and neighbours, where a write is one that has a
+// value or a state, since U itself may have become 0.
 // A single write far below the others is left alone: mostly their terms make the
 // output, and chance brings one in 10^4 chunks.  (Where a strong decay has emptied
 // those terms too, that one output, below 2^-28 of its neighbours', loses bits.)
-// Looking for all this costs 1 % (16 x 4096 x 16 heads 1195 -> 1204 us) to 2 %
-// (4 x 8192 x 6 heads 433 -> 442 us), at dk = 64 5 % (144 heads of 16 chunks 94 ->
-// 99 us).
-__device__ __forceinline__ bool below(float write, float largest) { return write != 0.0f && write < largest * 0x1p-28f; }
+// Looking for all this costs 1 % (16 x 4096 x 16 heads 1195 -> 1206 us, 4 x 8192 x
+// 6 heads 433 -> 438 us), at dk = 64 5 to 9 % (144 heads of 16 chunks 95 -> 99 us,
+// token-major rows 99 -> 107); a third look costs its CTA some 10 us.
 
 template <int DK, int VR, int VC>
 struct ScanStage {
@@ -735,6 +738,87 @@ __device__ __noinline__ void give_up(uint64_t* full, int ch, uint64_t budget_ns,
     const bf16 nan = __float2bfloat16_rn(__int_as_float(0x7fffffff));
     for (int c = 0; c < cols; ++c)
         for (int64_t t = t0 + int(threadIdx.x & 31); t < len; t += 32) o[c * channel + t * token] = nan;
+}
+
+// The second look at a chunk whose smallest write is small: without the tokens that write nothing (a write strength of 0,
+// behind the end).
+template <bool WIDE>
+__device__ __forceinline__ uint64_t strong_from(const Factors& f, int lane) {      // from this lane's first token on
+    return (uint64_t(f.strong[1]) << 32 | f.strong[0]) >> (WIDE ? 2 * (lane & 3) : lane >> 2);
+}
+template <bool WIDE, int J>
+__device__ __forceinline__ bool small_writes(const float (&U)[J][4], const Factors& f, int lane, float m0, float m1) {
+    const uint64_t strong = strong_from<WIDE>(f, lane);
+    float z0 = INFINITY, z1 = INFINITY;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (strong >> (WIDE ? 8 * j + i : 16 * j + 8 * i) & 1u) {
+                z0 = fminf(z0, fabsf(U[j][WIDE ? i : 2 * i]));
+                z1 = fminf(z1, fabsf(U[j][WIDE ? 2 + i : 2 * i + 1]));
+            }
+    return __any_sync(0xffffffffu, z0 < m0 * 0x1p-28f || z1 < m1 * 0x1p-28f);
+}
+
+// The third: what was said above, channel by channel.  U as the scans hold it (WIDE: element 2 c + i of tile j
+// is channel c, token 8 j + 2 t4 + i; else element 2 i + c, token 16 j + g + 8 i); v: this thread's first channel.
+struct Writes {
+    const Factors* f;
+    const bf16* v;
+    int v_channel, v_token;
+    float m[2], s[2];                              // as in Reach, by channel
+};
+template <bool WIDE, int J>
+__device__ __forceinline__ bool look_again(const float (&U)[J][4], const Writes& x) {
+    const int lane = int(threadIdx.x) & 31, g = lane >> 2, t4 = lane & 3;
+    auto token = [&](int j, int i) { return WIDE ? 8 * j + 2 * t4 + i : 16 * j + g + 8 * i; };
+    auto at = [](int c, int i) { return WIDE ? 2 * c + i : 2 * i + c; };
+    bool far = false;
+    const Reach reach = x.f->reach;
+    const float gamma = x.f->gamma;
+    const uint64_t strong = strong_from<WIDE>(*x.f, lane);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        // U may be 0 because it was too small: a token writes where there is a value or a state
+        unsigned live = 0;
+        int first = C;
+#pragma unroll
+        for (int j = J - 1; j >= 0; --j)
+#pragma unroll
+            for (int i = 1; i >= 0; --i) {
+                const int t = token(j, i);
+                if ((strong >> (t - token(0, 0)) & 1u) != 0 && (x.s[c] > 0.0f || __bfloat162float(x.v[c * x.v_channel + t * x.v_token]) != 0.0f)) {
+                    live |= 1u << (2 * j + i);
+                    first = t;
+                }
+            }
+#pragma unroll
+        for (int d = WIDE ? 1 : 4; d < (WIDE ? 4 : 32); d <<= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
+        const bool bare = reach.bare(x.m[c], x.s[c], gamma);
+        // neighbouring tokens: the other of this thread's two, or another lane's
+        const unsigned pair = WIDE ? live | (live >> 1 & 0x5555u) | (live << 1 & 0xaaaau) : live | __shfl_xor_sync(0xffffffffu, live, 4);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float own = fabsf(U[j][at(c, i)]);
+                const float other = WIDE ? fabsf(U[j][at(c, i ^ 1)]) : __shfl_xor_sync(0xffffffffu, own, 4);
+                far = far || (bare && (((pair >> (2 * j + i) & 1u) != 0 && fmaxf(own, other) < x.m[c] * 0x1p-28f) ||
+                                       (first == token(j, i) && own < x.m[c] * 0x1p-28f)));
+            }
+    }
+    return __any_sync(0xffffffffu, far);
+}
+// Called by the wide scan, for the same reason as chunk_by_token_apart.
+template <int J>
+__device__ __noinline__ bool look_again_apart(const float (&U)[J][4], const Writes& x) {
+    float own[J][4];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[j][i] = U[j][i];
+    return look_again<true>(own, x);
 }
 
 // One element of a tile of 16-bit numbers [token][channel], or (FIRST) [channel][token].
@@ -1028,30 +1112,16 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
         }
         const float u0 = quad_max(m0), u1 = quad_max(m1), w0 = quad_max(n0), w1 = quad_max(n1), gamma = f.gamma;
         const Reach reach = f.reach;
-        const bool end = reach.end(u0, r0, w0, s0, gamma) || reach.end(u1, r1, w1, s1, gamma);
-        if (n < C) {                               // behind the end nothing is written
-            z0 = z1 = INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (8 * nt + 2 * t4 + i < n) {
-                        z0 = fminf(z0, fabsf(U[nt][i]));
-                        z1 = fminf(z1, fabsf(U[nt][i + 2]));
-                    }
-        }
-        bool apart = __any_sync(0xffffffffu, end || z0 < u0 * 0x1p-28f || z1 < u1 * 0x1p-28f);
-        if (__builtin_expect(apart, 0)) {          // or tokens that write nothing, or one write by chance?
-            bool far = end;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float a0 = fabsf(U[nt][2 * c]), a1 = fabsf(U[nt][2 * c + 1]), u = c ? u1 : u0, s = c ? s1 : s0;
-                    far = far || below(fmaxf(a0, a1), u) || (reach.first == 8 * nt + 2 * t4 && reach.start(a0, u, s, gamma)) ||
-                          (reach.first == 8 * nt + 2 * t4 + 1 && reach.start(a1, u, s, gamma));
-                }
-            apart = __any_sync(0xffffffffu, far);
+        const float a0 = fmaxf(u0, r0 * reach.t), a1 = fmaxf(u1, r1 * reach.t);
+        const bool end = reach.end(a0, r0, w0, s0, gamma) || reach.end(a1, r1, w1, s1, gamma);
+        bool apart = __any_sync(0xffffffffu, end || z0 < a0 * 0x1p-28f || z1 < a1 * 0x1p-28f);
+        if (__builtin_expect(apart, 0) && !__any_sync(0xffffffffu, end)) {     // or tokens that write nothing, or chance?
+            apart = small_writes<true>(U, f, lane, a0, a1);
+            if (apart) {
+                float copy[8][4];
+                copy_state(copy, U);
+                apart = look_again_apart(copy, Writes{&f, &st.v[16 * warp + g][0], 8 * kVRow, 1, {a0, a1}, {s0, s1}});
+            }
         }
         if (__builtin_expect(apart, 0)) {
             state_by_token<DK, FIRST, true>(S, st.k, st.q, f, a, b, h, t0, n, &st.v[16 * warp + g][0], 8 * kVRow, 1,
@@ -1224,7 +1294,7 @@ __global__ void __launch_bounds__(32 * NW + kLoaders, 1) k_delta_scan(ChunkArgs 
 // so shared memory would bound more than four warps an SM.  A chunk takes 5500
 // cycles, the warp's and its scheduler's loading warp's issue slots two thirds
 // of them: 24 heads of 128 chunks 376 us (500 us with 16 channels a warp).  One
-// CTA an SM: 255 registers (dk = 64: 225) and half of the shared memory.
+// CTA an SM: 255 registers (dk = 64: 221) and half of the shared memory.
 constexpr int kNarrowWarps = 4, kNarrowCols = 8 * kNarrowWarps;
 constexpr int kNarrowVRow = kNarrowCols + 8;       // elements of a token's row of V: eight rows on 32 banks
 
@@ -1445,32 +1515,12 @@ __global__ void __launch_bounds__(32 * kNarrowWarps + kLoaders, 1) k_delta_scan_
         }
         const float u0 = column_max(m0), u1 = column_max(m1), w0 = column_max(n0), w1 = column_max(n1), gamma = f.gamma;
         const Reach reach = f.reach;
-        const bool end = reach.end(u0, r0, w0, s0, gamma) || reach.end(u1, r1, w1, s1, gamma);
-        if (n < C) {                               // behind the end nothing is written
-            z0 = z1 = INFINITY;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (16 * mt + g + 8 * i < n) {
-                        z0 = fminf(z0, fabsf(U[mt][2 * i]));
-                        z1 = fminf(z1, fabsf(U[mt][2 * i + 1]));
-                    }
-        }
-        bool apart = __any_sync(0xffffffffu, end || z0 < u0 * 0x1p-28f || z1 < u1 * 0x1p-28f);
-        if (__builtin_expect(apart, 0)) {          // or tokens that write nothing, or one write by chance?
-            bool far = end;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a0 = fabsf(U[mt][i]), u = (i & 1) ? u1 : u0, s = (i & 1) ? s1 : s0;
-                    const float a1 = __shfl_xor_sync(0xffffffffu, a0, 4);
-                    far = far || below(fmaxf(a0, a1), u) ||
-                          (reach.first == 16 * mt + g + 8 * (i >> 1) && reach.start(a0, u, s, gamma));
-                }
-            apart = __any_sync(0xffffffffu, far);
-        }
+        const float a0 = fmaxf(u0, r0 * reach.t), a1 = fmaxf(u1, r1 * reach.t);
+        const bool end = reach.end(a0, r0, w0, s0, gamma) || reach.end(a1, r1, w1, s1, gamma);
+        bool apart = __any_sync(0xffffffffu, end || z0 < a0 * 0x1p-28f || z1 < a1 * 0x1p-28f);
+        if (__builtin_expect(apart, 0) && !__any_sync(0xffffffffu, end))       // or tokens that write nothing, or chance?
+            apart = small_writes<false>(U, f, lane, a0, a1) &&
+                    look_again<false>(U, Writes{&f, &st.v[0][8 * warp + 2 * t4], 1, kNarrowVRow, {a0, a1}, {s0, s1}});
         if (__builtin_expect(apart, 0)) {
             state_by_token<DK, FIRST, false>(S, st.k, st.q, f, a, b, h, t0, n, &st.v[0][8 * warp + 2 * t4], 1, kNarrowVRow,
                                              so + 2 * t4 * (FIRST ? kVRow : 1), FIRST ? kVRow : 1, FIRST ? 1 : 8);

@@ -212,3 +212,65 @@ def test_far_apart_without_gate_tensors_and_with_a_scale(B, L, Hk, Hv, dk, dv, l
     ref = ro.reshape(B, Hv, dv, L)[:, :, 3, :40]
     mag, read = (x[:, :, 3, :40] * 0.25 * dk ** 0.5 for x in terms(c))
     assert (np.abs(early - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + STATE(dk, L) * read).all()
+
+
+@pytest.mark.parametrize("kind", ["values half zero", "every third token masked", "left 40 masked", "zero keys", "one token repeated",
+                                  "zeros, then small, then large", "masked, then small, then large", "all masked"])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("B,L,Hk,Hv,dk,dv", [(1, 150, 1, 2, 64, 64), (40, 66, 2, 4, 64, 64), (19, 100, 2, 4, 128, 128)])
+def test_tokens_that_write_nothing(B, L, Hk, Hv, dk, dv, state, kind):
+    """Exact zeros among the writes, alone and before a small write that a large one follows."""
+    c = Case(B, L, Hk, Hv, dk, dv, layout="last", state=state, decay=0.05)
+    v = c.v.unflatten(1, (Hv, dv))
+    groups = (slice(None),)
+    if kind == "values half zero":
+        c.v.relu_()
+    elif kind == "every third token masked":
+        c.beta[:, :, ::3] = 0
+    elif kind == "left 40 masked":
+        c.beta[:, :, :40] = 0
+    elif kind == "zero keys":
+        c.k[:, :, ::5] = 0
+    elif kind == "one token repeated":
+        c.k[:], c.v[:] = c.k[:, :, :1].clone(), c.v[:, :, :1].clone()
+        c.beta.fill_(1.0)
+    elif kind == "all masked":
+        c.beta.fill_(0.0)
+        if not state:                                     # nothing at all: zeros out
+            o, s1 = c.run()
+            assert (o == 0).all() and (s1 == 0).all()
+            return
+    else:
+        if kind.startswith("zeros"):
+            v[:, :, 9, :11] = 0
+        else:
+            c.beta[:, :, :11] = 0
+        v[:, :, 9, 12] = 1e14
+        groups = ([9], [d for d in range(dv) if d != 9])
+    check_tokens(c, *c.run(), groups=groups)
+
+
+@pytest.mark.parametrize("layout", ["first", "last"])
+@pytest.mark.parametrize("B,L,Hk,Hv,dk,dv", [(1, 17, 1, 2, 100, 64), (1, 81, 1, 2, 64, 64), (40, 66, 2, 4, 64, 64), (19, 100, 2, 4, 128, 128)])
+def test_large_value_masked_at_a_reset_on_the_last_token(B, L, Hk, Hv, dk, dv, layout):
+    """Nothing of the chunk remains behind it, and its largest residual writes nothing: the outputs before it still count."""
+    c = Case(B, L, Hk, Hv, dk, dv, layout=layout, decay=0.05)
+    c.v.unflatten(1, (Hv, dv))[:, :, :, L - 1] = 1e25
+    c.beta[:, :, L - 1] = 0.0
+    c.g[:, :, L - 1] = float("-inf")
+    ro, _ = c.oracle()
+    o, s1 = c.run()
+    assert (s1 == 0).all()
+    mag, read = (x.reshape(B, Hv * dv, L)[:, :, :-1] for x in terms(c))
+    err, ref = np.abs(_np(o) - ro)[:, :, :-1], np.abs(ro)[:, :, :-1]
+    assert (err <= 2.0 ** -8 * ref + 2.0 ** -10 * mag + STATE(dk, L) * read).all()
+
+
+@pytest.mark.parametrize("layout", ["first", "last"])
+@pytest.mark.parametrize("B,L,Hk,Hv,dk,dv", [(1, 150, 1, 2, 64, 64), (40, 66, 2, 4, 64, 64), (19, 100, 2, 4, 128, 128)])
+def test_masked_run_under_a_strong_decay(B, L, Hk, Hv, dk, dv, layout):
+    """Tokens that write nothing read what fades, by e^-10 a token, in their own size."""
+    c = Case(B, L, Hk, Hv, dk, dv, layout=layout, decay=0.05)
+    c.beta[:, :, 20:26] = 0.0
+    c.g[:, :, 20:26] = -10.0
+    check_tokens(c, *c.run())
